@@ -58,7 +58,12 @@ typedef enum {
   SVDQ_ERR_IO = 9               /* file could not be read or written         */
 } svdq_status;
 
-enum { SVDQ_EPI_NONE = 0, SVDQ_EPI_GELU = 1 };
+/* Epilogues.  SVDQ_EPI_SILU belongs to the 16-bit products (svdq_linear16);
+ * the quantised products take NONE and GELU. */
+enum { SVDQ_EPI_NONE = 0, SVDQ_EPI_GELU = 1, SVDQ_EPI_SILU = 2 };
+
+/* Element types of the 16-bit operators' arrays. */
+enum { SVDQ_DTYPE_BF16 = 0, SVDQ_DTYPE_F16 = 1, SVDQ_DTYPE_F32 = 2 };
 
 /* Number format of a packed handle: the W4A4 group format of every call
  * above, or the W8A8 comparator of svdq_pack_weights_w8a8. */
@@ -504,6 +509,166 @@ svdq_status svdq_quantize_act_nvfp4(const svdq_weights* w, int M, const uint16_t
 svdq_status svdq_linear_nvfp4(const svdq_weights* w, int M, const uint8_t* xq,
                               const uint8_t* sfa, const float* s_x, const uint16_t* Z,
                               uint16_t* Y, int ldy, int epilogue, cudaStream_t stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * 16-bit operators of a transformer block around the quantised layers: the
+ * linear layers that stay at 16 bits (review section 8 keeps the adaLN
+ * inputs and the cross-attention keys and values there), the layer norm in
+ * front of a quantised layer and the rotary positions behind the QKV
+ * product, each with its gradient.
+ *
+ * These calls take plain device arrays instead of a packed handle:
+ *   - element types are SVDQ_DTYPE_*; leading dimensions count elements;
+ *   - unless a call says otherwise, pointers and rows are 16-byte aligned,
+ *     else SVDQ_ERR_ALIGNMENT, while row lengths (K, N) may be any size: the
+ *     elements between a row's length and its leading dimension are neither
+ *     read nor written;
+ *   - the arrays are on the current device; outputs overlap no input and no
+ *     other output except where stated;
+ *   - calls are asynchronous on `stream`, allocate nothing and may be
+ *     captured into a graph; a workspace is needed only while its call runs,
+ *     and calls that share one must not overlap (graphs that were captured
+ *     with the same workspace included);
+ *   - sums, statistics and activations are fp32, outputs are rounded once.
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * 16-bit linear layer:  Y = epi(X W^T + b) + R.
+ *   X [M][ldx] (K columns), W [N][ldw] (nn.Linear layout, K columns),
+ *   b [N] or NULL, R [M][ldr] or NULL, Y [M][ldy], all of type `dtype`
+ *   (BF16 or F16); any M >= 0, K >= 1, N >= 1.
+ * epilogue: SVDQ_EPI_NONE, _GELU (exact-erf form) or _SILU, applied to the
+ * fp32 sum before R is added.
+ * P: [M][ldp] or NULL; receives X W^T + b rounded to `dtype`, the
+ * pre-activation that svdq_linear16_backward takes.
+ * R may be Y itself (R == Y with ldr == ldy: the product is added in place).
+ * A device wait that exceeds its bound raises the current device's sticky
+ * operator error word; read it with svdq_get_op_error.
+ */
+svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx,
+                          const void* W, int ldw, const void* bias, const void* R,
+                          int ldr, int epilogue, void* Y, int ldy, void* P, int ldp,
+                          cudaStream_t stream);
+
+/*
+ * Gradients of svdq_linear16 for the output gradient dY [M][lddy]:
+ *   dP = dY epi'(P) (rounded to `dtype`, the operand type of the products;
+ *        dP = dY when epilogue is NONE),
+ *   dX [M][lddx] = dP W,  dW [N][lddw] = dP^T X,  db [N] = sum_m dP (of the
+ *   fp32 values).  R's gradient is dY itself and is not copied.
+ * dX, dW and db may each be NULL (not computed); X is needed for dW only
+ * and W for dX only.  P [M][ldp] is the pre-activation that the forward call
+ * stored (ignored when epilogue is NONE).  M == 0 sets dW and db to zero.
+ * Results do not depend on timing: every sum has a fixed order.
+ * workspace: device memory, 256-byte aligned, of at least
+ * svdq_linear16_backward_workspace(M, K, N, epilogue) bytes; it needs no
+ * initialisation.
+ */
+size_t svdq_linear16_backward_workspace(int M, int K, int N, int epilogue);
+svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* dY, int lddy,
+                                   const void* X, int ldx, const void* W, int ldw,
+                                   const void* P, int ldp, int epilogue, void* dX, int lddx,
+                                   void* dW, int lddw, void* db, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Synchronises `stream`, then reads and clears the current device's operator
+ * error word: SVDQ_OK, or SVDQ_ERR_DEVICE_TIMEOUT if a bounded wait of a
+ * svdq_linear16 kernel expired on this device since the last read. */
+svdq_status svdq_get_op_error(cudaStream_t stream);
+
+#define SVDQ_NORM_MAX_K 16384
+
+/*
+ * Layer norm over rows of K elements, with a scale and a shift per group of
+ * rows (one group: the usual layer norm; one row of scale and shift per
+ * image: the modulated norm of diffusion transformers):
+ *   mu_i = mean(x_i),  rstd_i = 1 / sqrt(mean((x_i - mu_i)^2) + eps),
+ *   y_i  = (x_i - mu_i) rstd_i (w_g + weight_offset) + b_g,
+ *   g    = i / rows_per_group      (rows_per_group == 0: one group).
+ * X [M][ldx], Y [M][ldy] of `dtype` (BF16, F16 or F32); weight [groups][ldw]
+ * and bias [groups][ldb] of `param_dtype` (`dtype` or F32), each may be NULL
+ * (no scale: factor 1, weight_offset unused; no shift).  ldw and ldb may be 0
+ * (every group shares one row).  mean, rstd fp32 [M], each may be NULL:
+ * the statistics that the gradient takes.  Y may be X (with ldy == ldx).
+ * 1 <= K <= SVDQ_NORM_MAX_K, else SVDQ_ERR_UNSUPPORTED; eps finite and >= 0.
+ */
+svdq_status svdq_layer_norm(int dtype, int param_dtype, int M, int K, const void* X, int ldx,
+                            const void* weight, int ldw, const void* bias, int ldb,
+                            float weight_offset, int rows_per_group, float eps, void* Y,
+                            int ldy, float* mean, float* rstd, cudaStream_t stream);
+
+/*
+ * Gradients of svdq_layer_norm for dY [M][lddy] and the forward call's X,
+ * mean and rstd.  With xhat = (x - mu) rstd and t = dy (w_g + weight_offset):
+ *   dX  = rstd (t - mean(t) - xhat mean(t xhat)),
+ *   dweight_g = sum over the group's rows of dy xhat,  dbias_g = sum of dy.
+ * dX [M][lddx] of `dtype` may be dY or X itself (equal leading dimensions);
+ * dweight [groups][lddw] and dbias [groups][lddb] are of `param_dtype`.  dX,
+ * dweight and dbias may each be NULL (not computed).  groups =
+ * ceil(M / rows_per_group), one for rows_per_group == 0 (M == 0 then sets
+ * dweight and dbias to zero; with rows_per_group > 0 it has no group).
+ * The sums have a fixed order: results do not depend on timing.
+ * workspace: device memory, 256-byte aligned, of at least
+ * svdq_layer_norm_backward_workspace(M, K, rows_per_group) bytes (may be 0);
+ * it needs no initialisation and is unused when dweight and dbias are NULL.
+ */
+size_t svdq_layer_norm_backward_workspace(int M, int K, int rows_per_group);
+svdq_status svdq_layer_norm_backward(int dtype, int param_dtype, int M, int K, const void* dY,
+                                     int lddy, const void* X, int ldx, const float* mean,
+                                     const float* rstd, const void* weight, int ldw,
+                                     float weight_offset, int rows_per_group, void* dX,
+                                     int lddx, void* dweight, int lddw, void* dbias, int lddb,
+                                     void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+#define SVDQ_ROPE_MAX_AXES 4
+#define SVDQ_ROPE_MAX_PAIRS 128
+#define SVDQ_ROPE_MAX_HEADS 65535
+#define SVDQ_ROPE_MAX_HEAD_DIM 1024
+
+/* Which elements of a head form pair p of P: (2p, 2p + 1) or (p, P + p). */
+enum { SVDQ_ROPE_INTERLEAVED = 0, SVDQ_ROPE_HALVES = 1 };
+
+/* Rotary frequencies: host data, immutable, usable on every device. */
+typedef struct svdq_rope_plan svdq_rope_plan;
+
+/*
+ * Plan of rotary positions with several axes (time, height and width of
+ * images and video): axis a turns pairs_per_axis[a] consecutive pairs, and
+ * pair p of axis a is turned by the angle position[a] freq[p] (radians).
+ * n_axes 1 .. SVDQ_ROPE_MAX_AXES, pairs_per_axis[a] >= 0 with 1 ..
+ * SVDQ_ROPE_MAX_PAIRS pairs in all (SVDQ_ERR_SHAPE otherwise); freq host fp64
+ * [pairs], finite, below 2^20 in magnitude (SVDQ_ERR_NUMERIC otherwise).  A
+ * frequency is kept as a 64-bit fraction of a turn, so that its product with
+ * a 32-bit position is exact modulo one turn and the angle of a far position
+ * is as accurate as that of a near one.
+ */
+svdq_status svdq_rope_create(int n_axes, const int* pairs_per_axis, const double* freq,
+                             int pairing, svdq_rope_plan** out);
+void svdq_rope_free(svdq_rope_plan* plan);
+
+/*
+ * Rotates every head of every token:
+ *   (a, b) -> (a cos - b sin, a sin + b cos) for each pair, the angle's sign
+ *   reversed when `inverse` is not 0 (the gradient of the rotation).
+ * X, Y: element (t, h, d) at t * ld_token + h * ld_head + d, type `dtype`
+ * (BF16, F16 or F32), d < head_dim, which is even and at least twice the
+ * plan's pairs; elements past the pairs are copied.  At most
+ * SVDQ_ROPE_MAX_HEADS heads of SVDQ_ROPE_MAX_HEAD_DIM elements, else
+ * SVDQ_ERR_UNSUPPORTED.  Pointers and strides need only element alignment
+ * (16-byte aligned ones are faster).  Heads and tokens of Y do not share
+ * elements; Y may be X with equal strides (in place).  positions: device int32 [pos_rows][ld_pos], one
+ * column per axis, any sign; token t uses row t % pos_rows (images of one
+ * size in a batch share their positions).  Queries and keys side by side in
+ * the rows of a fused QKV product are one call over their heads.
+ */
+svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int heads,
+                      int head_dim, const int32_t* positions, int pos_rows, int ld_pos,
+                      const void* X, long long ldx_token, long long ldx_head, void* Y,
+                      long long ldy_token, long long ldy_head, int inverse,
+                      cudaStream_t stream);
 
 #ifdef __cplusplus
 }

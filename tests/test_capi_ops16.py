@@ -1,0 +1,185 @@
+"""CPU checks of the 16-bit operators' calls: every refusal is a status code
+returned before anything touches a GPU, empty calls succeed, workspace
+queries are consistent, and the binding rejects unfit tensors."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import w4a4_quantized_gemm_smooth_b200 as S
+
+vp = ctypes.c_void_p
+OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, NUMERIC = 0, 1, 2, 3, 4, 5
+# aligned addresses that no refused call reads
+A, B, C, D, E, F, G = (0x10000 * (i + 1) for i in range(7))
+
+
+def linear(dtype=0, M=8, K=64, N=32, X=A, ldx=64, W=B, ldw=64, bias=None, R=None, ldr=0, epi=0, Y=C,
+           ldy=32, P=None, ldp=0):
+    return S.lib().svdq_linear16(dtype, M, K, N, X, ldx, W, ldw, bias, R, ldr, epi, Y, ldy, P, ldp, None)
+
+
+def test_linear16_refusals():
+    assert linear(M=0) == OK
+    assert linear(dtype=2) == INVALID and linear(dtype=-1) == INVALID
+    assert linear(epi=3) == INVALID and linear(epi=-1) == INVALID
+    assert linear(M=-1) == SHAPE and linear(K=0) == SHAPE and linear(N=0) == SHAPE
+    assert linear(ldx=56) == SHAPE and linear(ldw=56) == SHAPE and linear(ldy=24) == SHAPE
+    assert linear(R=D, ldr=24) == SHAPE and linear(P=D, ldp=24) == SHAPE
+    assert linear(M=0x7FFFFFFF) == UNSUPPORTED
+    for k in ("X", "W", "Y"):
+        assert linear(**{k: None}) == INVALID
+        assert linear(**{k: 0x10008}) == ALIGN
+    assert linear(P=C, ldp=32) == INVALID                       # P and Y are one array
+    assert linear(R=D, ldr=32, P=D, ldp=32) == INVALID
+    assert linear(R=C, ldr=40, ldy=32) == INVALID               # in place with another pitch
+    assert linear(bias=0x10002) == ALIGN
+    assert linear(R=0x10008, ldr=32) == ALIGN and linear(P=0x10008, ldp=32) == ALIGN
+    assert linear(ldx=66) == ALIGN and linear(ldw=66) == ALIGN and linear(ldy=34) == ALIGN
+    assert linear(R=D, ldr=34) == ALIGN and linear(P=D, ldp=34) == ALIGN
+
+
+def linear_bwd(dtype=0, M=8, K=64, N=32, dY=A, lddy=32, X=B, ldx=64, W=C, ldw=64, P=D, ldp=32, epi=1,
+               dX=E, lddx=64, dW=F, lddw=64, db=G, ws=0x100000, nbytes=1 << 30):
+    return S.lib().svdq_linear16_backward(dtype, M, K, N, dY, lddy, X, ldx, W, ldw, P, ldp, epi, dX,
+                                          lddx, dW, lddw, db, ws, nbytes, None)
+
+
+def test_linear16_backward_refusals():
+    assert linear_bwd(dX=None, dW=None, db=None) == OK          # nothing is asked for
+    assert linear_bwd(dtype=2) == INVALID and linear_bwd(epi=3) == INVALID
+    assert linear_bwd(M=-1) == SHAPE and linear_bwd(K=0) == SHAPE and linear_bwd(N=0) == SHAPE
+    assert linear_bwd(lddy=24) == SHAPE and linear_bwd(ldx=56) == SHAPE and linear_bwd(ldw=56) == SHAPE
+    assert linear_bwd(ldp=24) == SHAPE and linear_bwd(lddx=56) == SHAPE and linear_bwd(lddw=56) == SHAPE
+    assert linear_bwd(N=0x7FFFFFFF, lddy=0x7FFFFFFF, ldp=0x7FFFFFFF) == UNSUPPORTED
+    for k in ("dY", "X", "W", "P", "ws"):
+        assert linear_bwd(**{k: None}) == INVALID
+    for k in ("dY", "X", "W", "P", "dX", "dW"):
+        assert linear_bwd(**{k: 0x10008}) == ALIGN
+    assert linear_bwd(ws=0x100080) == ALIGN and linear_bwd(db=0x10001) == ALIGN
+    need = S.svdq_linear16_backward_workspace(8, 64, 32, S.EPI_GELU)
+    assert linear_bwd(nbytes=need - 1) == SHAPE
+    assert S.svdq_linear16_backward_workspace(8, 64, 32, 3) == 0
+    assert S.svdq_linear16_backward_workspace(0, 64, 32) == 0
+    # dP of an activation is held in the workspace, rows padded to 16 bytes
+    assert S.svdq_linear16_backward_workspace(1000, 64, 33, S.EPI_SILU) >= 1000 * 40 * 2
+
+
+def norm(dtype=0, pt=0, M=4, K=64, X=A, ldx=64, w=B, ldw=64, b=C, ldb=64, off=0.0, rpg=2, eps=1e-6,
+         Y=D, ldy=64, mean=None, rstd=None):
+    return S.lib().svdq_layer_norm(dtype, pt, M, K, X, ldx, w, ldw, b, ldb, off, rpg, eps, Y, ldy, mean,
+                                   rstd, None)
+
+
+def test_layer_norm_refusals():
+    assert norm(M=0) == OK
+    assert norm(dtype=3) == INVALID and norm(dtype=0, pt=1) == INVALID and norm(dtype=2, pt=0) == INVALID
+    for eps in (-1e-6, math.nan, math.inf):
+        assert norm(eps=eps) == INVALID
+    assert norm(off=math.nan) == INVALID
+    assert norm(M=-1) == SHAPE and norm(K=0) == SHAPE and norm(rpg=-1) == SHAPE
+    assert norm(ldx=56) == SHAPE and norm(ldy=56) == SHAPE and norm(ldw=56) == SHAPE and norm(ldb=56) == SHAPE
+    assert norm(K=16385, ldx=16392, ldy=16392, ldw=16392, ldb=16392) == UNSUPPORTED
+    assert norm(X=None) == INVALID and norm(Y=None) == INVALID
+    assert norm(Y=A, ldy=72) == INVALID                          # in place with another pitch
+    for k in ("X", "Y", "w", "b"):
+        assert norm(**{k: 0x10004}) == ALIGN
+    assert norm(ldx=66) == ALIGN and norm(ldy=66) == ALIGN and norm(ldw=66) == ALIGN and norm(ldb=66) == ALIGN
+    assert norm(mean=0x10002) == ALIGN and norm(rstd=0x10001) == ALIGN
+
+
+def norm_bwd(dtype=0, pt=2, M=4096, K=64, dY=A, lddy=64, X=B, ldx=64, mean=C, rstd=C, w=D, ldw=64, off=0.0,
+             rpg=0, dX=E, lddx=64, dw=F, lddw=64, db=G, lddb=64, ws=0x100000, nbytes=1 << 30):
+    return S.lib().svdq_layer_norm_backward(dtype, pt, M, K, dY, lddy, X, ldx, mean, rstd, w, ldw, off, rpg,
+                                            dX, lddx, dw, lddw, db, lddb, ws, nbytes, None)
+
+
+def test_layer_norm_backward_refusals():
+    assert norm_bwd(dX=None, dw=None, db=None) == OK
+    assert norm_bwd(M=0, rpg=2) == OK                            # no group, nothing to write
+    assert norm_bwd(dtype=0, pt=1) == INVALID and norm_bwd(off=math.inf) == INVALID
+    assert norm_bwd(M=-1) == SHAPE and norm_bwd(K=0) == SHAPE and norm_bwd(rpg=-1) == SHAPE
+    for k in ("lddy", "ldx", "ldw", "lddx", "lddw", "lddb"):
+        assert norm_bwd(**{k: 56}) == SHAPE
+    assert norm_bwd(K=16385, **{k: 16392 for k in ("lddy", "ldx", "ldw", "lddx", "lddw", "lddb")}) == UNSUPPORTED
+    for k in ("dY", "X", "mean", "rstd", "ws"):
+        assert norm_bwd(**{k: None}) == INVALID
+    assert norm_bwd(dX=A, lddx=72) == INVALID and norm_bwd(dX=B, lddx=72) == INVALID
+    for k in ("dY", "X", "w", "dX", "dw", "db"):
+        assert norm_bwd(**{k: 0x10004}) == ALIGN
+    assert norm_bwd(ws=0x100010) == ALIGN and norm_bwd(mean=0x10002) == ALIGN
+    need = S.svdq_layer_norm_backward_workspace(4096, 64, 0)
+    assert need > 0 and norm_bwd(nbytes=need - 1) == SHAPE
+    assert S.svdq_layer_norm_backward_workspace(4, 64, 1) == 0   # one row per group: no partial sums
+    assert S.svdq_layer_norm_backward_workspace(4, 16385, 1) == 0
+
+
+def plan(pairs=(8, 28, 28), freq=None, pairing=0, n=None):
+    pp = np.asarray(pairs, np.int32)
+    fr = np.asarray(np.ones(max(int(pp.clip(0).sum()), 1)) if freq is None else freq, np.float64)
+    h = vp()
+    rc = S.lib().svdq_rope_create(len(pp) if n is None else n, pp.ctypes.data_as(vp), fr.ctypes.data_as(vp),
+                                  pairing, ctypes.byref(h))
+    assert (rc == OK) == bool(h.value)
+    return rc, h
+
+
+def test_rope_plan_refusals():
+    assert plan(n=0)[0] == INVALID and plan((1,) * 5)[0] == INVALID and plan(pairing=2)[0] == INVALID
+    assert plan((0, 0))[0] == SHAPE and plan((-1, 3))[0] == SHAPE and plan((100, 29))[0] == SHAPE
+    for f in (math.nan, math.inf, 2.0 ** 20, -2.0 ** 20):
+        assert plan((1,), [f])[0] == NUMERIC
+    assert S.lib().svdq_rope_create(1, None, None, 0, ctypes.byref(vp())) == INVALID
+    for f in (0.0, -1.0, 1.0, 2 * math.pi, 1e-30):
+        rc, h = plan((1,), [f])
+        assert rc == OK
+        S.lib().svdq_rope_free(h)
+    S.lib().svdq_rope_free(None)
+
+
+def test_rope_refusals():
+    _, h = plan()
+
+    def rope(dtype=0, T=4, H=2, D=128, pos=A, rows=4, ldp=3, X=B, xt=256, xh=128, Y=C, yt=256, yh=128, p=h):
+        return S.lib().svdq_rope(p, dtype, T, H, D, pos, rows, ldp, X, xt, xh, Y, yt, yh, 0, None)
+
+    assert rope(T=0) == OK and rope(H=0) == OK
+    assert rope(p=None) == INVALID and rope(dtype=3) == INVALID
+    assert rope(T=-1) == SHAPE and rope(H=-1) == SHAPE and rope(rows=0) == SHAPE and rope(ldp=2) == SHAPE
+    assert rope(D=126) == SHAPE and rope(D=129, yh=129) == SHAPE and rope(D=0) == SHAPE
+    assert rope(xt=-1) == SHAPE and rope(xh=-1) == SHAPE and rope(yt=-1) == SHAPE and rope(yh=-1) == SHAPE
+    assert rope(yh=64) == SHAPE and rope(yt=64) == SHAPE         # heads or tokens of Y overlap
+    assert rope(D=1026, yh=1026, yt=4000) == UNSUPPORTED and rope(H=65536) == UNSUPPORTED
+    assert rope(pos=None) == INVALID and rope(X=None) == INVALID and rope(Y=None) == INVALID
+    assert rope(X=B, Y=B, yt=512) == INVALID                     # in place with other strides
+    assert rope(X=0x10001) == ALIGN and rope(Y=0x10001) == ALIGN and rope(pos=0x10002) == ALIGN
+    assert rope(dtype=2, X=0x10002) == ALIGN
+    S.lib().svdq_rope_free(h)
+
+
+def test_binding_rejects_unfit_tensors():
+    x = torch.zeros((4, 8), dtype=torch.bfloat16)
+    w = torch.zeros((16, 8), dtype=torch.bfloat16)
+    y = torch.zeros((4, 16), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        S.svdq_linear16(x, w, y)
+    with pytest.raises(ValueError, match="CUDA"):
+        S.svdq_layer_norm(x, x)
+    with pytest.raises(ValueError, match="dtype"):
+        S.svdq_layer_norm(x.double(), x.double())
+    with pytest.raises(ValueError, match="frequency"):
+        S.svdq_rope_create([2, 2], [1.0])
+    p = S.svdq_rope_create([2, 2], S.rope_frequencies([2, 2]))
+    with pytest.raises(ValueError):
+        S.svdq_rope(p, torch.zeros((4, 2), dtype=torch.int64), torch.zeros(4, 1, 8), torch.zeros(4, 1, 8))
+    with pytest.raises(ValueError):
+        S.svdq_rope(p, torch.zeros((4, 2), dtype=torch.int32), torch.zeros(4, 8), torch.zeros(4, 8))
+    p.free()
+    p.free()
+
+
+def test_rope_frequencies():
+    assert S.rope_frequencies([2, 4], 100.0) == pytest.approx(
+        [1.0, 0.1, 1.0, 100.0 ** -0.25, 0.1, 100.0 ** -0.75], rel=1e-15)

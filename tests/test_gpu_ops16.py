@@ -1,0 +1,686 @@
+"""GPU checks of the 16-bit operators against plain 64-bit forms.
+
+Every tolerance is a bound, not a fit.  With h = finfo(dtype).eps / 2, the
+half step of the output's rounding, an output may be off by h |y| plus what
+fp32 arithmetic loses before it:
+  products    n 2^-24 sum |terms| for a sum of n products (any order), times
+              the activation's steepest slope (1.13 for GELU, 1.1 for SiLU),
+              2^-20 |p| for the activation itself, 2^-23 (|y| + |r|) for the
+              last additions;
+  layer norm  a row's sums go through at most 80 additions in a row (48 per
+              thread at most, then the tree), so they are off by 80 2^-24 of
+              the sum of magnitudes;
+  rotations   2^-22 (|a| + |b|): the angle's 2^-25 half turns (9.4e-8) and the
+              sine's and cosine's own 2^-23, then two products and a sum.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import w4a4_quantized_gemm_smooth_b200 as S
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+SLOPE = {S.EPI_NONE: 1.0, S.EPI_GELU: 1.13, S.EPI_SILU: 1.1}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "gpu tests need a CUDA device"
+    S.lib()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rows(g, m, k, dtype, scale=1.0, ld=None, guard=None):
+    """[m, k] values in rows of ld elements; the padding holds `guard`."""
+    ld = ld or -(-k // 8) * 8
+    x = torch.full((m, ld), float("nan") if guard is None else guard, dtype=dtype, device="cuda")
+    x[:, :k] = (torch.randn((m, k), generator=g, device="cuda") * scale).to(dtype)
+    return x[:, :k]
+
+
+def out(m, k, dtype, ld=None):
+    """[m, k] to be written, in rows whose padding holds 77."""
+    return torch.full((m, ld or -(-k // 8) * 8 + 8), 77.0, dtype=dtype, device="cuda")[:, :k]
+
+
+def padding_kept(y):
+    base = y._base
+    return bool((base[:, y.shape[1]:] == 77.0).all())
+
+
+def half(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def close(y, ref, tol, what=""):
+    d = (y.double() - ref).abs()
+    tiny = 2.0 ** -25 if y.dtype == F16 else 1e-37
+    bad = ~(d <= tol + tiny)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((d / (tol + tiny)).nan_to_num(1e9).max()):.3g} x the bound"
+
+
+def act64(p, epi):
+    if epi == S.EPI_GELU:
+        return p * torch.special.ndtr(p)
+    return p * torch.sigmoid(p) if epi == S.EPI_SILU else p
+
+
+def act_grad64(p, epi):
+    if epi == S.EPI_GELU:
+        return torch.special.ndtr(p) + p * torch.exp(-p * p / 2) / (2 * torch.pi) ** 0.5
+    if epi == S.EPI_SILU:
+        q = torch.sigmoid(p)
+        return q * (1 + p * (1 - q))
+    return torch.ones_like(p)
+
+
+# ------------------------------------------------------------------- linear
+def check_linear(M, K, N, dtype, epi, bias=True, res=True, pre=True, seed=0, inplace=False):
+    g = gen(seed)
+    X, W = rows(g, M, K, dtype), rows(g, N, K, dtype, K ** -0.5)
+    b = torch.randn((N,), generator=g, device="cuda").to(dtype) if bias else None
+    Y, P = out(M, N, dtype), out(M, N, dtype) if pre else None
+    R = rows(g, M, N, dtype) if res else None
+    r64 = R.double() if res else 0.0
+    if inplace:
+        Y.copy_(R)
+        R = Y
+    S.svdq_linear16(X, W, Y, b, R, epi, P)
+    S.svdq_get_op_error()
+    x, w = X.double(), W.double()
+    p = x @ w.T + (b.double() if bias else 0.0)
+    e_p = (K + 1) * 2.0 ** -24 * (x.abs() @ w.abs().T + (b.double().abs() if bias else 0.0))
+    a = act64(p, epi)
+    y = a + r64
+    e = SLOPE[epi] * e_p + (2.0 ** -20 * p.abs() if epi else 0.0) + 2.0 ** -23 * (a.abs() + (r64.abs() if res else 0.0))
+    h = half(dtype)
+    close(Y, y, h * (y.abs() + e) + e, "Y")
+    assert padding_kept(Y)
+    if pre:
+        close(P, p, h * (p.abs() + e_p) + e_p, "P")
+        assert padding_kept(P)
+
+
+@pytest.mark.parametrize("M,K,N", [
+    (1, 1, 1), (1, 8, 8), (1, 64, 128), (2, 65, 7), (3, 1152, 6912), (8, 1153, 130), (16, 200, 96),
+    (17, 4608, 1152), (64, 256, 512), (127, 333, 257), (128, 128, 128), (129, 129, 129),
+    (200, 64, 1000), (256, 1152, 1152), (300, 100, 2307), (1000, 520, 72), (777, 1153, 385),
+])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_linear_sizes(M, K, N, dtype):
+    check_linear(M, K, N, dtype, S.EPI_GELU, seed=M + K + N)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("epi", [S.EPI_NONE, S.EPI_GELU, S.EPI_SILU])
+@pytest.mark.parametrize("bias,res,pre", [(False, False, False), (True, False, False), (False, True, False),
+                                          (False, False, True), (True, True, True)])
+@pytest.mark.parametrize("M", [1, 150])
+def test_linear_epilogues(dtype, epi, bias, res, pre, M):
+    check_linear(M, 328, 301, dtype, epi, bias, res, pre, seed=5)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 1152, 640), (40, 300, 200), (500, 700, 1200)])
+def test_linear_residual_in_place(M, K, N):
+    check_linear(M, K, N, BF16, S.EPI_NONE, inplace=True, pre=False, seed=9)
+
+
+@pytest.mark.parametrize("M,K,N,dtype", [(4096, 1152, 4608, BF16), (2500, 4608, 1160, F16), (5000, 72, 9216, BF16),
+                                         (20000, 128, 264, BF16)])
+def test_linear_many_tiles(M, K, N, dtype):
+    check_linear(M, K, N, dtype, S.EPI_SILU, seed=3)
+
+
+def test_linear_strides_and_column_views():
+    """Operands and output as column slices of wider arrays."""
+    g = gen(1)
+    wide = rows(g, 100, 512, BF16)
+    X, W = wide[:, 64:64 + 128], rows(g, 48, 128, BF16, 0.1, ld=200)
+    buf = torch.full((100, 256), 77.0, dtype=BF16, device="cuda")
+    S.svdq_linear16(X, W, buf[:, 96:144])
+    ref = X.double() @ W.double().T
+    e = 128 * 2.0 ** -24 * (X.double().abs() @ W.double().abs().T)
+    close(buf[:, 96:144], ref, half(BF16) * (ref.abs() + e) + e)
+    assert bool((buf[:, :96] == 77).all()) and bool((buf[:, 144:] == 77).all())
+
+
+@pytest.mark.parametrize("M", [1, 5, 70, 300])
+def test_linear_rows_are_independent(M):
+    """A row with NaN or infinities spoils its own output row only."""
+    g = gen(2)
+    X, W = rows(g, M, 200, BF16), rows(g, 136, 200, BF16, 0.1)
+    Y0, Y1 = out(M, 136, BF16), out(M, 136, BF16)
+    S.svdq_linear16(X, W, Y0)
+    bad = X.clone()
+    bad[M // 2, 3] = float("nan")
+    if M > 1:
+        bad[0, 5] = float("inf")
+    S.svdq_linear16(bad, W, Y1)
+    touched = torch.zeros(M, dtype=torch.bool, device="cuda")
+    touched[M // 2] = True
+    touched[0] |= M > 1
+    assert torch.equal(Y0[~touched], Y1[~touched])
+    assert bool(Y1[M // 2].isnan().all())
+    if M > 1:
+        assert not bool(Y1[0].isfinite().any())
+
+
+def test_linear_extreme_activations():
+    """Pre-activations far outside, infinite and NaN through both activations."""
+    v = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 12.0, -12.0, 90.0, -90.0, 3e4, -3e4,
+                      float("inf"), float("-inf"), float("nan"), -1e38], device="cuda").to(BF16)
+    X = torch.zeros((16, 8), dtype=BF16, device="cuda")
+    X[:, 0] = v
+    W = torch.zeros((8, 8), dtype=BF16, device="cuda")
+    W[0, 0] = 1.0
+    for epi, at_minus_inf in ((S.EPI_GELU, float("nan")), (S.EPI_SILU, float("nan"))):
+        Y = out(16, 8, BF16)
+        S.svdq_linear16(X, W, Y, epilogue=epi)
+        y, ref = Y[:, 0].double(), act64(v.double(), epi)
+        fin = v.isfinite()
+        assert bool((y[fin] - ref[fin]).abs().le(half(BF16) * ref[fin].abs() + 2.0 ** -20 * v[fin].double().abs()).all())
+        assert bool(y[12].isposinf()) and bool(y[14].isnan())
+        # -inf times a zero factor: no finite value can be right, and 0 is the limit
+        assert bool(y[13].isnan()) or float(y[13]) == 0.0
+
+
+def check_linear_bwd(M, K, N, dtype, epi, bias=True, seed=0, want=(True, True, True)):
+    g = gen(seed)
+    X, W = rows(g, M, K, dtype), rows(g, N, K, dtype, K ** -0.5)
+    dY, P = rows(g, M, N, dtype), rows(g, M, N, dtype, 1.5)
+    dX, dW = out(M, K, dtype) if want[0] else None, out(N, K, dtype) if want[1] else None
+    db = torch.full((N,), 77.0, dtype=dtype, device="cuda") if want[2] else None
+    ws = torch.empty((max(S.svdq_linear16_backward_workspace(M, K, N, epi), 1),), dtype=torch.uint8, device="cuda")
+    S.svdq_linear16_backward(dY, X, W, P if epi else None, dX, dW, db, ws, epi)
+    S.svdq_get_op_error()
+    x, w, d = X.double(), W.double(), dY.double()
+    h = half(dtype)
+    dp = d * act_grad64(P.double(), epi) if epi else d
+    # the fp32 slope is good to 2^-20 of its largest value, 1.13; dP is then an operand of 16 bits
+    e32 = 2.0 ** -20 * d.abs() if epi else torch.zeros_like(d)
+    tiny = 2.0 ** -25 if dtype == F16 else 0.0
+    e16 = e32 + h * (dp.abs() + e32) + tiny if epi else e32
+    m = dp.abs() + e16
+    if want[0]:
+        ref = dp @ w
+        e = e16 @ w.abs() + N * 2.0 ** -24 * (m @ w.abs())
+        close(dX, ref, h * (ref.abs() + e) + e, "dX")
+        assert padding_kept(dX)
+    if want[1]:
+        ref = dp.T @ x
+        e = e16.T @ x.abs() + M * 2.0 ** -24 * (m.T @ x.abs())
+        close(dW, ref, h * (ref.abs() + e) + e, "dW")
+        assert padding_kept(dW)
+    if want[2]:
+        ref = dp.sum(0)
+        e = e32.sum(0) + M * 2.0 ** -24 * m.sum(0)
+        close(db, ref, h * (ref.abs() + e) + e, "db")
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 200, 136), (2, 65, 7), (33, 72, 300), (64, 64, 64), (129, 130, 131),
+                                   (333, 1153, 77), (777, 200, 1001), (1000, 1152, 320)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("epi", [S.EPI_NONE, S.EPI_GELU, S.EPI_SILU])
+def test_linear_backward(M, K, N, dtype, epi):
+    check_linear_bwd(M, K, N, dtype, epi, seed=M)
+
+
+@pytest.mark.parametrize("M,K,N,dtype", [(4096, 1152, 1160, BF16), (9000, 136, 400, F16)])
+def test_linear_backward_long(M, K, N, dtype):
+    check_linear_bwd(M, K, N, dtype, S.EPI_GELU, seed=8)
+
+
+@pytest.mark.parametrize("want", [(True, False, False), (False, True, False), (False, False, True)])
+@pytest.mark.parametrize("epi", [S.EPI_NONE, S.EPI_SILU])
+def test_linear_backward_parts(want, epi):
+    check_linear_bwd(100, 136, 72, BF16, epi, want=want)
+
+
+def test_linear_backward_of_an_empty_batch_is_zero():
+    dW, db = out(24, 40, BF16), torch.full((24,), 77.0, dtype=BF16, device="cuda")
+    e = lambda k: torch.empty((0, k), dtype=BF16, device="cuda")
+    W = torch.ones((24, 40), dtype=BF16, device="cuda")
+    S.svdq_linear16_backward(e(24), e(40), W, None, e(40), dW, db, None)
+    assert bool((dW == 0).all()) and bool((db == 0).all()) and padding_kept(dW)
+
+
+def test_linear_gradients_against_differences():
+    """Central differences of the 64-bit loss sum(Y dY) through the GPU's own
+    forward pass would drown in 16-bit steps, so the differences are of the
+    64-bit formula at the GPU's pre-activation."""
+    g = gen(11)
+    M, K, N = 40, 72, 56
+    X, W = rows(g, M, K, F16), rows(g, N, K, F16, 0.1)
+    b = torch.randn((N,), generator=g, device="cuda").to(F16)
+    dY = rows(g, M, N, F16)
+    layer = S.Linear16(W, b, S.EPI_GELU)
+    layer.forward(X, save=True)
+    dX, dW, db = layer.backward(dY)
+    loss = lambda x, w, c: (act64(x @ w.T + c, S.EPI_GELU) * dY.double()).sum()
+    x, w, c, t = X.double(), W.double(), b.double(), 1e-5
+    for grad, k in ((dX, 0), (dW, 1), (db, 2)):
+        d = torch.randn(grad.shape, generator=g, device="cuda", dtype=torch.float64)
+        at = lambda s: loss(*[v + s * t * d if i == k else v for i, v in enumerate((x, w, c))])
+        num = float((at(1) - at(-1)) / (2 * t))
+        # P is rounded to fp16 (slope changes by at most 0.8 2^-11 |p|), dP and the result once each
+        scale = float((grad.double().abs() * d.abs()).sum())
+        assert abs(float((grad.double() * d).sum()) - num) <= 4 * 2.0 ** -11 * scale
+
+
+# --------------------------------------------------------------- layer norm
+def norm64(X, w, b, eps, off, rpg):
+    x = X.double()
+    mu = x.mean(1, keepdim=True)
+    d = x - mu
+    rstd = ((d * d).mean(1, keepdim=True) + eps).rsqrt()
+    y = d * rstd
+    grp = torch.arange(X.shape[0], device="cuda") // (rpg or max(X.shape[0], 1))
+    ww = (w.double()[grp] if w.dim() == 2 else w.double()[None]) + off if w is not None else torch.ones_like(x[:1])
+    bb = (b.double()[grp] if b.dim() == 2 else b.double()[None]) if b is not None else torch.zeros_like(x[:1])
+    return x, mu, d, rstd, y, ww, bb, grp
+
+
+def check_norm(M, K, dtype, pt, groups=1, off=0.0, affine=True, offset=0.0, seed=0, eps=1e-6, inplace=False):
+    g = gen(seed)
+    X = rows(g, M, K, dtype)
+    X += torch.tensor(offset, dtype=dtype, device="cuda")
+    rpg = -(-M // groups) if groups > 1 else 0
+    used = -(-M // rpg) if rpg else 1
+    w = rows(g, used, K, pt, 0.3, guard=5.0) if affine else None
+    b = rows(g, used, K, pt, 0.3, guard=5.0) if affine else None
+    if affine and groups == 1:
+        w, b = w[0], b[0]
+    x, mu, d, rstd, y0, ww, bb, _ = norm64(X, w, b, eps, off, rpg)
+    Y = out(M, K, dtype)
+    if inplace:
+        Y.copy_(X)
+    mean, rs = torch.empty((M,), device="cuda"), torch.empty((M,), device="cuda")
+    S.svdq_layer_norm(Y if inplace else X, Y, w, b, eps, off, rpg, mean, rs)
+    u = 2.0 ** -24
+    e_d = 80 * u * x.abs().mean(1, keepdim=True) + u * d.abs()
+    sd = (d * d).mean(1, keepdim=True) + eps
+    e_r = 0.5 * (84 * u + (e_d * e_d).mean(1, keepdim=True) / sd + 2 * (e_d * d.abs() * u).mean(1, keepdim=True) / sd
+                 + 2 * 80 * u * x.abs().mean(1, keepdim=True) * 80 * u * d.abs().mean(1, keepdim=True) / sd) + 3 * u
+    y = y0 * ww + bb
+    e = rstd * ww.abs() * e_d * 1.001 + (y0 * ww).abs() * (e_r + 4 * u) + 2 * u * (y.abs() + bb.abs())
+    h = half(dtype)
+    close(Y, y, h * (y.abs() + e) + e, "Y")
+    assert padding_kept(Y)
+    close(mean, mu[:, 0], 81 * u * x.abs().mean(1), "mean")
+    close(rs, rstd[:, 0], (rstd * (e_r + u))[:, 0], "rstd")
+
+
+SIZES = [(1, 1), (1, 2), (3, 7), (5, 8), (2, 63), (4, 64), (7, 255), (129, 256), (130, 257), (33, 768), (6, 1152),
+         (1000, 1152), (9, 1281), (40, 2049), (20, 3073), (17, 4608), (5, 5121), (3, 8193), (2, 12288), (2, 16384)]
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("dtype,pt", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32), (F32, F32)])
+def test_norm_sizes(M, K, dtype, pt):
+    check_norm(M, K, dtype, pt, seed=M + K)
+
+
+@pytest.mark.parametrize("M,K,groups", [(8, 72, 8), (10, 1152, 3), (1000, 136, 4), (7, 4608, 7), (5, 520, 2)])
+@pytest.mark.parametrize("off", [0.0, 1.0])
+def test_norm_groups(M, K, groups, off):
+    check_norm(M, K, BF16, BF16, groups, off, seed=K)
+    check_norm(M, K, F32, F32, groups, off, seed=K)
+
+
+@pytest.mark.parametrize("offset", [100.0, -3000.0])
+@pytest.mark.parametrize("K", [64, 1153, 9000])
+def test_norm_large_mean(offset, K):
+    """A mean far above the spread: the variance must not cancel."""
+    check_norm(12, K, F32, F32, offset=offset, affine=False)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("affine", [False, True])
+def test_norm_plain_and_in_place(inplace, affine):
+    check_norm(100, 1152, BF16, BF16, affine=affine, inplace=inplace)
+    check_norm(9, 2500, F16, F32, affine=affine, inplace=inplace)
+
+
+def test_norm_constant_and_bad_rows():
+    """Constant rows give the shift exactly; NaN and infinity stay in their row."""
+    X = torch.randn((6, 200), device="cuda")
+    X[1] = 3.0
+    X[2] = 0.0
+    X[3, 7] = float("nan")
+    X[4, 9] = float("inf")
+    w, b = torch.randn((200,), device="cuda"), torch.randn((200,), device="cuda")
+    Y, Z = torch.empty_like(X), torch.empty_like(X)
+    S.svdq_layer_norm(X, Y, w, b)
+    assert torch.equal(Y[1], b) and torch.equal(Y[2], b)
+    assert bool(Y[3].isnan().all()) and bool(Y[4].isnan().all())
+    X[3], X[4] = 1.0, 2.0
+    S.svdq_layer_norm(X, Z, w, b)
+    assert torch.equal(Y[[0, 1, 2, 5]], Z[[0, 1, 2, 5]])
+
+
+def test_norm_of_no_rows():
+    e = torch.empty((0, 64), dtype=BF16, device="cuda")
+    S.svdq_layer_norm(e, e)
+    dw = torch.full((64,), 7.0, dtype=BF16, device="cuda")
+    z = torch.empty((0,), device="cuda")
+    S.svdq_layer_norm_backward(e, e, z, z, e, dweight=dw)
+    assert bool((dw == 0).all())
+
+
+def check_norm_bwd(M, K, dtype, pt, groups=1, off=0.0, affine=True, seed=0, want=(True, True, True), alias=None):
+    g = gen(seed)
+    X, dY = rows(g, M, K, dtype), rows(g, M, K, dtype)
+    X += 0.5
+    rpg = -(-M // groups) if groups > 1 else 0
+    used = -(-M // rpg) if rpg else 1
+    w = rows(g, used, K, pt, 0.3, guard=5.0) if affine else None
+    x, mu, d, rstd, _, ww, _, grp = norm64(X, w, None, 1e-6, off, rpg)
+    mean, rs = mu[:, 0].float(), rstd[:, 0].float()
+    dX = out(M, K, dtype) if want[0] else None
+    if alias:
+        dX.copy_(X if alias == "X" else dY)
+    dw, db = (out(used, K, pt) if f else None for f in want[1:])
+    n = S.svdq_layer_norm_backward_workspace(M, K, rpg)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None
+    S.svdq_layer_norm_backward(dX if alias == "dY" else dY, dX if alias == "X" else X, mean, rs, dX, w, off, rpg,
+                               dw, db, ws)
+    u = 2.0 ** -24
+    r = rs.double()[:, None]
+    h = (x - mean.double()[:, None]) * r
+    dy = dY.double()
+    t = dy * ww
+    th = t * h
+    m1, m2 = t.mean(1, keepdim=True), th.mean(1, keepdim=True)
+    eps_h = half(dtype)
+    if want[0]:
+        ref = r * (t - m1 - h * m2)
+        e = r * (4 * u * t.abs() + 84 * u * t.abs().mean(1, keepdim=True)
+                 + h.abs() * 90 * u * th.abs().mean(1, keepdim=True) + 6 * u * ((h * m2).abs() + m1.abs()))
+        close(dX, ref, eps_h * (ref.abs() + e) + e, "dX")
+        assert padding_kept(dX)
+    hp = half(pt)
+    zero = torch.zeros((used, K), dtype=torch.float64, device="cuda")
+    count = torch.bincount(grp, minlength=used)[:, None]
+    for got, terms, name in ((dw, dy * h, "dweight"), (db, dy, "dbias")):
+        if got is not None:
+            ref = zero.index_add(0, grp, terms)
+            e = (count + 3) * u * zero.index_add(0, grp, terms.abs())
+            close(got, ref, hp * (ref.abs() + e) + e, name)
+            assert padding_kept(got)
+
+
+@pytest.mark.parametrize("M,K", SIZES + [(5000, 64), (3000, 1152), (1500, 4608), (700, 9216)])
+@pytest.mark.parametrize("dtype,pt", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32), (F32, F32)])
+def test_norm_backward_sizes(M, K, dtype, pt):
+    check_norm_bwd(M, K, dtype, pt, seed=M + K)
+
+
+@pytest.mark.parametrize("M,K,groups", [(8, 72, 8), (10, 1152, 3), (1000, 136, 4), (7, 4608, 7), (2000, 520, 2),
+                                        (1100, 1153, 5)])
+@pytest.mark.parametrize("off", [0.0, 1.0])
+def test_norm_backward_groups(M, K, groups, off):
+    check_norm_bwd(M, K, BF16, BF16, groups, off, seed=K)
+    check_norm_bwd(M, K, F32, F32, groups, off, seed=K)
+
+
+@pytest.mark.parametrize("want", [(True, False, False), (False, True, False), (False, False, True), (False, True, True)])
+@pytest.mark.parametrize("K", [200, 2000, 9000])
+def test_norm_backward_parts(want, K):
+    check_norm_bwd(300, K, BF16, F32, want=want)
+
+
+@pytest.mark.parametrize("alias", ["X", "dY"])
+@pytest.mark.parametrize("K", [200, 2000, 9000])
+def test_norm_backward_in_place(alias, K):
+    check_norm_bwd(50, K, BF16, F32, alias=alias)
+
+
+def test_norm_backward_without_weight():
+    check_norm_bwd(300, 1152, BF16, BF16, affine=False, want=(True, False, False))
+    # the sums do not need the weight
+    check_norm_bwd(300, 1152, BF16, BF16, affine=False)
+
+
+def test_norm_gradients_against_differences():
+    g = gen(4)
+    M, K, rpg = 12, 96, 5
+    X, dY = rows(g, M, K, F32), rows(g, M, K, F32)
+    w, b = rows(g, 3, K, F32), rows(g, 3, K, F32)
+    layer = S.LayerNorm(w, b, 1e-5, 1.0)
+    layer.forward(X, rows_per_group=rpg, save=True)
+    dX, dw, db = layer.backward(dY)
+
+    def loss(x, ww, bb):
+        grp = torch.arange(M, device="cuda") // rpg
+        d = x - x.mean(1, keepdim=True)
+        y = d * ((d * d).mean(1, keepdim=True) + 1e-5).rsqrt() * (ww[grp] + 1.0) + bb[grp]
+        return (y * dY.double()).sum()
+
+    at0, t = (X.double(), w.double(), b.double()), 1e-5
+    for grad, k in ((dX, 0), (dw, 1), (db, 2)):
+        d = torch.randn(grad.shape, generator=g, device="cuda", dtype=torch.float64)
+        at = lambda s: loss(*[v + s * t * d if i == k else v for i, v in enumerate(at0)])
+        num = float((at(1) - at(-1)) / (2 * t))
+        scale = float((grad.double().abs() * d.abs()).sum())
+        assert abs(float((grad.double() * d).sum()) - num) <= 2.0 ** -17 * scale
+
+
+# --------------------------------------------------------------------- rope
+def rope64(X, pos, pairs, freq, pairing, inverse):
+    n = len(freq)
+    axis = torch.tensor([a for a, p in enumerate(pairs) for _ in range(p)], device="cuda")
+    f = torch.tensor(freq, dtype=torch.float64, device="cuda")
+    rowi = torch.arange(X.shape[0], device="cuda") % pos.shape[0]
+    ang = pos[rowi].double()[:, axis] * f * (-1.0 if inverse else 1.0)
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+    x, y = X.double(), X.double().clone()
+    ia, ib = ((slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if pairing == S.ROPE_INTERLEAVED
+              else (slice(0, n), slice(n, 2 * n)))
+    a, b = x[..., ia], x[..., ib]
+    y[..., ia], y[..., ib] = a * c - b * s, a * s + b * c
+    mag = torch.zeros_like(y)
+    mag[..., ia] = mag[..., ib] = a.abs() + b.abs()
+    return y, mag
+
+
+def check_rope(T, H, D, pairs, pairing, dtype, inverse=False, far=1000, pad=0, head_pad=0, shift=0, prows=None,
+               inplace=False, seed=0, freq=None):
+    g = gen(seed)
+    xt = H * (D + head_pad) + pad
+    buf = torch.randn((T * xt + shift,), generator=g, device="cuda").to(dtype)
+    view = lambda v: v[shift:].view(T, xt)[:, :H * (D + head_pad)].unflatten(1, (H, D + head_pad))[..., :D]
+    X = view(buf)
+    obuf = buf.clone() if inplace else torch.full_like(buf, 77.0)
+    O = view(obuf)
+    pos = torch.randint(-far, far, (prows or T, len(pairs)), generator=g, device="cuda", dtype=torch.int32)
+    freq = freq or S.rope_frequencies(pairs)
+    plan = S.svdq_rope_create(pairs, freq, pairing)
+    S.svdq_rope(plan, pos, O if inplace else X, O, inverse)
+    ref, mag = rope64(X, pos, pairs, freq, pairing, inverse)
+    e = 2.0 ** -22 * mag
+    n = 2 * len(freq)
+    # the 64-bit reference's own angle is good to 2^-53 of its size
+    e = e + 2.0 ** -52 * far * max(abs(f) for f in freq) * mag
+    close(O, ref, half(dtype) * (ref.abs() + e) + e, "rope")
+    assert torch.equal(O[..., n:], X[..., n:])
+    kept = torch.ones_like(obuf, dtype=torch.bool)
+    view(kept).fill_(False)
+    assert torch.equal(obuf[kept], (buf if inplace else torch.full_like(buf, 77.0))[kept])
+
+
+@pytest.mark.parametrize("pairing", [S.ROPE_INTERLEAVED, S.ROPE_HALVES])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,H,D,pairs", [
+    (1, 1, 2, (1,)), (1, 48, 128, (8, 28, 28)), (5, 3, 8, (2, 2)), (7, 2, 72, (12, 12, 12)), (9, 5, 64, (10, 10, 8)),
+    (33, 4, 38, (3, 8, 8)), (100, 9, 42, (15, 2)), (20, 2, 256, (32, 48, 48)), (3, 1, 1024, (128,)), (50, 1, 6, (1, 0, 1)),
+])
+def test_rope_sizes(T, H, D, pairs, pairing, dtype):
+    check_rope(T, H, D, pairs, pairing, dtype, seed=T + D)
+    check_rope(T, H, D, pairs, pairing, dtype, inverse=True, pad=24, seed=T)
+
+
+@pytest.mark.parametrize("pairing", [S.ROPE_INTERLEAVED, S.ROPE_HALVES])
+@pytest.mark.parametrize("shift,pad,head_pad", [(1, 0, 0), (2, 3, 0), (4, 4, 4), (0, 1, 0), (0, 0, 1), (3, 5, 7)])
+def test_rope_any_alignment(shift, pad, head_pad, pairing):
+    for dtype in (BF16, F32):
+        check_rope(11, 3, 48, (8, 8, 4), pairing, dtype, shift=shift, pad=pad, head_pad=head_pad)
+
+
+@pytest.mark.parametrize("pairing", [S.ROPE_INTERLEAVED, S.ROPE_HALVES])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rope_far_positions(pairing, dtype):
+    check_rope(64, 3, 128, (8, 28, 28), pairing, dtype, far=2 ** 31 - 1)
+    check_rope(64, 2, 16, (4, 4), pairing, dtype, far=2 ** 20, freq=[1.0, -2.5, 3e-9, 0.0, 100.0, 7.5, 1e-3, 6.0])
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_rope_shared_positions_and_in_place(inplace):
+    check_rope(60, 6, 72, (12, 12, 12), S.ROPE_HALVES, BF16, prows=15, inplace=inplace, pad=216)
+    check_rope(60, 6, 96, (12, 12, 12), S.ROPE_INTERLEAVED, BF16, prows=60, inplace=inplace, pad=288)
+
+
+def test_rope_many_heads_and_tokens():
+    check_rope(4608, 64, 128, (8, 28, 28), S.ROPE_INTERLEAVED, BF16, far=64)
+    check_rope(2, 1000, 8, (4,), S.ROPE_HALVES, F16)
+    check_rope(70000, 1, 8, (1, 1), S.ROPE_INTERLEAVED, F16)
+
+
+def test_rope_copies_what_it_does_not_turn():
+    """NaN and infinity past the pairs pass through; inside a pair they stay in it."""
+    X = torch.randn((4, 2, 24), device="cuda").to(BF16)
+    X[:, :, 10:] = float("inf")
+    X[1, 1, 12] = float("nan")
+    X[2, 0, 0] = float("nan")
+    for pairing, mates in ((S.ROPE_INTERLEAVED, [0, 1]), (S.ROPE_HALVES, [0, 5])):
+        plan = S.svdq_rope_create([5], S.rope_frequencies([5]), pairing)
+        Y = torch.empty_like(X)
+        S.svdq_rope(plan, torch.arange(4, dtype=torch.int32, device="cuda")[:, None], X, Y)
+        assert torch.equal(Y[..., 10:].view(torch.int16), X[..., 10:].view(torch.int16))
+        bad = Y[..., :10].isnan().nonzero().tolist()
+        assert bad == [[2, 0, m] for m in mates]
+
+
+def test_rope_inverse_undoes_it_and_is_the_gradient():
+    g = gen(6)
+    X, G = torch.randn((30, 4, 40), generator=g, device="cuda"), torch.randn((30, 4, 40), generator=g, device="cuda")
+    pos = torch.randint(0, 10 ** 6, (30, 2), generator=g, device="cuda", dtype=torch.int32)
+    plan = S.svdq_rope_create([8, 8], S.rope_frequencies([8, 8]))
+    Y, B, GX = torch.empty_like(X), torch.empty_like(X), torch.empty_like(X)
+    S.svdq_rope(plan, pos, X, Y)
+    S.svdq_rope(plan, pos, Y, B, inverse=True)
+    assert float((B - X).abs().max()) <= 2 * 2.0 ** -21 * float(X.abs().max())
+    S.svdq_rope(plan, pos, G, GX, inverse=True)       # <R x, g> = <x, R^T g>
+    lhs, rhs = float((Y.double() * G.double()).sum()), float((X.double() * GX.double()).sum())
+    assert abs(lhs - rhs) <= 2.0 ** -20 * float((Y.double() * G.double()).abs().sum())
+
+
+# ------------------------------------------------- streams, graphs, together
+def test_calls_on_a_side_stream_and_in_a_graph():
+    """Captured and replayed calls on new inputs give the eager bits."""
+    g = gen(21)
+    M, K, N = 130, 200, 264
+    X, W, dY = rows(g, M, K, BF16), rows(g, N, K, BF16, 0.1), rows(g, M, N, BF16)
+    lin, norm = S.Linear16(W, torch.zeros((N,), dtype=BF16, device="cuda"), S.EPI_SILU), \
+        S.LayerNorm(torch.ones((K,), device="cuda"), torch.zeros((K,), device="cuda"))
+    plan = S.svdq_rope_create([2, 2], S.rope_frequencies([2, 2]))
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")[:, None].repeat(1, 2)
+    R = torch.empty((M, 33, 8), dtype=BF16, device="cuda")
+
+    def step():
+        n = norm(X, save=True)
+        y = lin(n, save=True)
+        dn, dW, db = lin.backward(dY)
+        dx, dw, dbn = norm.backward(dn)
+        S.svdq_rope(plan, pos, y.unflatten(1, (33, 8)), R)
+        return [y, dn, dW, db, dx, dw, dbn, R]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for t in step():
+            pass
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    X.copy_(torch.randn((M, K), generator=g, device="cuda"))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in captured]
+    eager = step()
+    torch.cuda.synchronize()
+    for a, b in zip(got, eager):
+        assert torch.equal(a, b)
+    S.svdq_get_op_error()
+
+
+def test_results_repeat_bit_for_bit():
+    g = gen(22)
+    X, W, dY, P = rows(g, 3000, 200, F16), rows(g, 136, 200, F16, 0.1), rows(g, 3000, 136, F16), rows(g, 3000, 136, F16)
+    ws = torch.empty((S.svdq_linear16_backward_workspace(3000, 200, 136, S.EPI_GELU),), dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(5):
+        Y, dX, dW, db = out(3000, 136, F16), out(3000, 200, F16), out(136, 200, F16), torch.empty((136,), dtype=F16, device="cuda")
+        S.svdq_linear16(X, W, Y, epilogue=S.EPI_GELU)
+        S.svdq_linear16_backward(dY, X, W, P, dX, dW, db, ws, S.EPI_GELU)
+        now = [Y, dX, dW, db]
+        if first is not None:
+            assert all(torch.equal(a, b) for a, b in zip(first, now))
+        first = now
+
+
+def test_calls_from_other_threads_and_streams():
+    """Concurrent calls with their own buffers do not disturb one another."""
+    import threading
+    g = gen(23)
+    jobs = [(rows(g, 70 + 40 * i, 264, BF16), rows(g, 200, 264, BF16, 0.1)) for i in range(4)]
+    want = []
+    for X, W in jobs:
+        Y = out(X.shape[0], 200, BF16)
+        S.svdq_linear16(X, W, Y)
+        want.append(Y)
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    Y = out(jobs[i][0].shape[0], 200, BF16)
+                    S.svdq_linear16(jobs[i][0], jobs[i][1], Y)
+                torch.cuda.current_stream().synchronize()
+            got[i] = Y
+        except Exception as e:      # handed to the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_status_codes_reach_python():
+    X = torch.zeros((4, 64), dtype=BF16, device="cuda")
+    W = torch.zeros((8, 64), dtype=BF16, device="cuda")
+    Y = torch.zeros((4, 8), dtype=BF16, device="cuda")
+    with pytest.raises(S.SVDQError) as e:
+        S.svdq_linear16(X, W, Y, epilogue=7)
+    assert e.value.status == 1
+    with pytest.raises(S.SVDQError) as e:
+        S.svdq_linear16(torch.zeros((4, 70), dtype=BF16, device="cuda")[:, 3:67], W, Y)
+    assert e.value.status == 3
+    with pytest.raises(ValueError):
+        S.svdq_linear16(X, W.to(F16), Y)
+    with pytest.raises(ValueError):
+        S.svdq_linear16(X, W, Y.T)
+    with pytest.raises(ValueError):
+        S.svdq_linear16(X, W, Y, bias=torch.zeros((7,), dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError):
+        S.svdq_layer_norm(X, X, torch.zeros((3, 64), dtype=BF16, device="cuda"), rows_per_group=1)

@@ -13,10 +13,16 @@ The call names follow include/svdq.h:
     the W8A8 comparator svdq_pack_weights_w8a8, svdq_quantize_act_w8a8,
     svdq_linear_w8a8, and the NVFP4 variant svdq_pack_weights_nvfp4,
     svdq_quantize_act_nvfp4, svdq_linear_nvfp4, and the cross-layer fusion
-    svdq_linear_quantize_next
+    svdq_linear_quantize_next,
+    the 16-bit operators around the quantised layers svdq_linear16,
+    svdq_layer_norm, svdq_rope (with svdq_rope_create) and the gradients
+    svdq_linear16_backward, svdq_layer_norm_backward, and svdq_get_op_error
 and SVDQLinear / W8A8Linear / NVFP4Linear bundle one packed layer with its
 two hot-path calls; SVDQMLP chains two layers (fc1, GELU, fc2) with or
-without the fusion.
+without the fusion, behind a layer norm if one is given; SVDQQKV chains a
+norm, a packed QKV layer and the rotary positions of its queries and keys;
+Linear16 and LayerNorm bundle a 16-bit operator with its buffers and its
+gradient.
 """
 from __future__ import annotations
 
@@ -35,12 +41,19 @@ __all__ = [
     "svdq_quantize_act_nvfp4", "svdq_linear_nvfp4", "svdq_nvfp4_sf_bytes", "NVFP4Linear",
     "svdq_linear_quantize_next", "svdq_linear_quantize_next_workspace", "SVDQMLP",
     "svdq_linear_host", "svdq_linear_host_workspace",
+    "EPI_SILU", "svdq_linear16", "svdq_linear16_backward", "svdq_linear16_backward_workspace",
+    "svdq_get_op_error", "svdq_layer_norm", "svdq_layer_norm_backward",
+    "svdq_layer_norm_backward_workspace", "ROPE_INTERLEAVED", "ROPE_HALVES", "RopePlan",
+    "svdq_rope_create", "svdq_rope", "rope_frequencies", "Linear16", "LayerNorm", "SVDQQKV",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libsvdq.so")
 EPI_NONE = 0
 EPI_GELU = 1
+EPI_SILU = 2        # 16-bit products only
+ROPE_INTERLEAVED = 0
+ROPE_HALVES = 1
 FORMAT_W4A4 = 0
 FORMAT_W8A8 = 1
 FORMAT_NVFP4 = 2
@@ -117,6 +130,22 @@ def lib() -> ctypes.CDLL:
         "svdq_linear_quantize_next_workspace": (ctypes.c_size_t, [_vp, _vp, _i]),
         "svdq_linear_quantize_next": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp,
                                            ctypes.c_size_t, _vp]),
+        "svdq_linear16": (_i, [_i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _i, _vp,
+                               _i, _vp]),
+        "svdq_linear16_backward_workspace": (ctypes.c_size_t, [_i, _i, _i, _i]),
+        "svdq_linear16_backward": (_i, [_i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _i,
+                                        _vp, _i, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
+        "svdq_get_op_error": (_i, [_vp]),
+        "svdq_layer_norm": (_i, [_i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _i, ctypes.c_float, _i,
+                                 ctypes.c_float, _vp, _i, _vp, _vp, _vp]),
+        "svdq_layer_norm_backward_workspace": (ctypes.c_size_t, [_i, _i, _i]),
+        "svdq_layer_norm_backward": (_i, [_i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i,
+                                          ctypes.c_float, _i, _vp, _i, _vp, _i, _vp, _i, _vp,
+                                          ctypes.c_size_t, _vp]),
+        "svdq_rope_create": (_i, [_i, _vp, _vp, _i, _vp]),
+        "svdq_rope_free": (None, [_vp]),
+        "svdq_rope": (_i, [_vp, _i, _i, _i, _i, _vp, _i, _i, _vp, ctypes.c_longlong,
+                           ctypes.c_longlong, _vp, ctypes.c_longlong, ctypes.c_longlong, _i, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -452,6 +481,263 @@ def svdq_debug_partials(w: Weights, M, xq, row0, nrows, col0, ncols, P, stream=N
            "svdq_debug_partials")
 
 
+# ------------------------------------------------------------------------
+# 16-bit operators around the quantised layers.  These calls take plain
+# tensors, so the binding checks each one's device, type and shape before it
+# passes the pointer on (ValueError); the library checks sizes and alignment.
+
+_DTYPES: dict = {}
+
+
+def _dtype_code(t, name="X"):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported")
+    return code
+
+
+def _raw_stream(stream, t):
+    """The stream's handle; None: the current stream of t's device, which has
+    to be the current device (launches go there)."""
+    import torch
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the tensors have to be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream
+
+
+def _matrix(t, name, rows, cols, like):
+    """(pointer, leading dimension) of a [rows, cols] tensor on like's device,
+    of like's type."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+    ld = t.stride(0)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows have to be contiguous")
+    if rows <= 1:
+        ld = -(-cols // 8) * 8          # a single row has no pitch
+    return t.data_ptr(), ld
+
+
+def _vector(t, name, n, like, dtype=None):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected {n} contiguous values")
+    if t.dtype != (dtype or like.dtype) or t.device != like.device:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype or like.dtype} on {like.device}")
+    return t.data_ptr()
+
+
+def _workspace(ws, like):
+    if ws is None:
+        return None, 0
+    if ws.device != like.device or not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on the operands' device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def svdq_linear16(X, W, Y, bias=None, residual=None, epilogue=EPI_NONE, preact=None, stream=None):
+    """Y = epi(X W^T + bias) + residual.  X [M, K], W [N, K], Y [M, N], all
+    cuda bf16 or fp16 with contiguous rows; bias [N]; residual [M, N] (may be
+    Y); preact [M, N] receives X W^T + bias for svdq_linear16_backward."""
+    code = _dtype_code(X)
+    M, K = X.shape
+    N = W.shape[0]
+    st = _raw_stream(stream, X)
+    x, ldx = _matrix(X, "X", M, K, X)
+    w, ldw = _matrix(W, "W", N, K, X)
+    y, ldy = _matrix(Y, "Y", M, N, X)
+    b = None if bias is None else _vector(bias, "bias", N, X)
+    r, ldr = (None, 0) if residual is None else _matrix(residual, "residual", M, N, X)
+    p, ldp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, X)
+    _check(lib().svdq_linear16(code, M, K, N, x, ldx, w, ldw, b, r, ldr, epilogue, y, ldy, p, ldp,
+                               st), "svdq_linear16")
+
+
+def svdq_linear16_backward_workspace(M: int, K: int, N: int, epilogue=EPI_NONE) -> int:
+    """Workspace bytes of svdq_linear16_backward (0 for invalid arguments)."""
+    return int(lib().svdq_linear16_backward_workspace(int(M), int(K), int(N), int(epilogue)))
+
+
+def svdq_linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue=EPI_NONE,
+                           stream=None):
+    """Gradients of svdq_linear16: dX [M, K], dW [N, K] and dbias [N] (each may
+    be None) for dY [M, N]; preact is the forward call's (None without an
+    activation).  The residual's gradient is dY itself."""
+    code = _dtype_code(dY, "dY")
+    M, N = dY.shape
+    K = X.shape[1] if X is not None else W.shape[1]
+    st = _raw_stream(stream, dY)
+    d, ldd = _matrix(dY, "dY", M, N, dY)
+    opt = lambda t, name, r, c: (None, 0) if t is None else _matrix(t, name, r, c, dY)
+    x, ldx = opt(X, "X", M, K)
+    w, ldw = opt(W, "W", N, K)
+    p, ldp = opt(preact, "preact", M, N)
+    gx, ldgx = opt(dX, "dX", M, K)
+    gw, ldgw = opt(dW, "dW", N, K)
+    gb = None if dbias is None else _vector(dbias, "dbias", N, dY)
+    ws, nbytes = _workspace(workspace, dY)
+    _check(lib().svdq_linear16_backward(code, M, K, N, d, ldd, x, ldx, w, ldw, p, ldp, epilogue,
+                                        gx, ldgx, gw, ldgw, gb, ws, nbytes, st),
+           "svdq_linear16_backward")
+
+
+def svdq_get_op_error(stream=None):
+    """Synchronises the stream and raises if a bounded wait of a 16-bit
+    operator expired on the current device since the last call."""
+    _check(lib().svdq_get_op_error(_stream_ptr(stream)), "device")
+
+
+def _params(t, name, groups, K, like, shared=True):
+    """(pointer, leading dimension) of a parameter [groups, K] or [K] (shared
+    by every group) and its type's code."""
+    if t.device != like.device or t.shape[-1] != K or t.dim() not in (1, 2) or \
+            (K > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: expected [{groups}, {K}] or [{K}] with contiguous rows on {like.device}")
+    if t.dim() == 1 or t.shape[0] == 1:
+        if not shared and groups != 1:
+            raise ValueError(f"{name}: expected [{groups}, {K}]")
+        return t.data_ptr(), 0 if shared else -(-K // 8) * 8
+    if t.shape[0] != groups:
+        raise ValueError(f"{name}: expected {groups} rows")
+    return t.data_ptr(), t.stride(0)
+
+
+def _param_code(X, *ps):
+    """The parameters' common type code (X's type or float32)."""
+    ts = [p for p in ps if p is not None]
+    if not ts:
+        return _dtype_code(X)
+    if any(p.dtype != ts[0].dtype for p in ts):
+        raise ValueError("the parameters and their gradients have to be of one type")
+    return _dtype_code(ts[0], "parameter")
+
+
+def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, rows_per_group=0,
+                    mean=None, rstd=None, stream=None):
+    """Y = (X - mean) rstd (weight + weight_offset) + bias over rows of X
+    [M, K] (bf16, fp16 or fp32).  weight, bias: [K], or [groups, K] with one
+    row for every rows_per_group rows of X; X's type or fp32.  mean, rstd:
+    fp32 [M], the statistics for svdq_layer_norm_backward.  Y may be X."""
+    import torch
+    code = _dtype_code(X)
+    M, K = X.shape
+    st = _raw_stream(stream, X)
+    x, ldx = _matrix(X, "X", M, K, X)
+    y, ldy = _matrix(Y, "Y", M, K, X)
+    pc = _param_code(X, weight, bias)
+    groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
+    w, ldw = (None, 0) if weight is None else _params(weight, "weight", groups, K, X)
+    b, ldb = (None, 0) if bias is None else _params(bias, "bias", groups, K, X)
+    mu = None if mean is None else _vector(mean, "mean", M, X, torch.float32)
+    rs = None if rstd is None else _vector(rstd, "rstd", M, X, torch.float32)
+    _check(lib().svdq_layer_norm(code, pc, M, K, x, ldx, w, ldw, b, ldb, weight_offset,
+                                 rows_per_group, eps, y, ldy, mu, rs, st), "svdq_layer_norm")
+
+
+def svdq_layer_norm_backward_workspace(M: int, K: int, rows_per_group: int = 0) -> int:
+    """Workspace bytes of svdq_layer_norm_backward (may be 0)."""
+    return int(lib().svdq_layer_norm_backward_workspace(int(M), int(K), int(rows_per_group)))
+
+
+def svdq_layer_norm_backward(dY, X, mean, rstd, dX, weight=None, weight_offset=0.0,
+                             rows_per_group=0, dweight=None, dbias=None, workspace=None,
+                             stream=None):
+    """Gradients of svdq_layer_norm: dX [M, K] (may be dY or X), dweight and
+    dbias [groups, K] or, with one group, [K]; each may be None."""
+    import torch
+    code = _dtype_code(X)
+    M, K = X.shape
+    st = _raw_stream(stream, X)
+    d, ldd = _matrix(dY, "dY", M, K, X)
+    x, ldx = _matrix(X, "X", M, K, X)
+    gx, ldgx = (None, 0) if dX is None else _matrix(dX, "dX", M, K, X)
+    pc = _param_code(X, weight, dweight, dbias)
+    groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
+    w, ldw = (None, 0) if weight is None else _params(weight, "weight", groups, K, X)
+    gw, ldgw = (None, 0) if dweight is None else _params(dweight, "dweight", groups, K, X, False)
+    gb, ldgb = (None, 0) if dbias is None else _params(dbias, "dbias", groups, K, X, False)
+    mu = _vector(mean, "mean", M, X, torch.float32)
+    rs = _vector(rstd, "rstd", M, X, torch.float32)
+    ws, nbytes = _workspace(workspace, X)
+    _check(lib().svdq_layer_norm_backward(code, pc, M, K, d, ldd, x, ldx, mu, rs, w, ldw,
+                                          weight_offset, rows_per_group, gx, ldgx, gw, ldgw, gb,
+                                          ldgb, ws, nbytes, st), "svdq_layer_norm_backward")
+
+
+class RopePlan:
+    """Owns one rotary-position plan (svdq_rope_plan*): host data only."""
+
+    def __init__(self, handle, n_axes: int, pairs: int):
+        self._h = handle
+        self.n_axes, self.pairs = n_axes, pairs
+
+    @property
+    def handle(self):
+        return self._h
+
+    def free(self):
+        if self._h:
+            lib().svdq_rope_free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def rope_frequencies(pairs_per_axis, theta: float = 10000.0) -> list:
+    """The usual frequencies, theta^(-i / p) for pair i of an axis of p pairs."""
+    return [float(theta) ** (-i / p) for p in pairs_per_axis for i in range(p)]
+
+
+def svdq_rope_create(pairs_per_axis, freq, pairing=ROPE_INTERLEAVED) -> RopePlan:
+    """Plan of rotary positions: axis a turns pairs_per_axis[a] consecutive
+    pairs of a head; freq holds every pair's frequency (radians per position)."""
+    pp = np.ascontiguousarray(pairs_per_axis, dtype=np.int32)
+    fr = np.ascontiguousarray(freq, dtype=np.float64)
+    if pp.ndim != 1 or fr.ndim != 1 or fr.shape[0] != int(pp.sum()):
+        raise ValueError("freq: expected one frequency per pair")
+    h = _vp()
+    _check(lib().svdq_rope_create(len(pp), _np_ptr(pp), _np_ptr(fr), int(pairing),
+                                  ctypes.byref(h)), "svdq_rope_create")
+    return RopePlan(h, len(pp), len(fr))
+
+
+def svdq_rope(plan: RopePlan, positions, X, out, inverse=False, stream=None):
+    """Rotates the heads of X [T, H, D] (bf16, fp16 or fp32, any token and
+    head strides) into out (same shape; X itself rotates in place).
+    positions: int32 [T, axes], or [R, axes] shared by tokens t with equal
+    t % R.  inverse: the opposite rotation, the gradient of the first."""
+    import torch
+    code = _dtype_code(X)
+    if X.dim() != 3 or out.shape != X.shape or out.dtype != X.dtype or out.device != X.device:
+        raise ValueError("X and out: expected [tokens, heads, head_dim] of one type and device")
+    T, H, D = X.shape
+    if D > 1 and (X.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("X and out: a head's elements have to be contiguous")
+    if positions.dim() != 2 or positions.shape[1] != plan.n_axes or \
+            positions.dtype != torch.int32 or positions.device != X.device or \
+            (plan.n_axes > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions: expected int32 [rows, {plan.n_axes}] on {X.device}")
+    R = positions.shape[0]
+    ldp = positions.stride(0) if R > 1 else plan.n_axes
+    st = _raw_stream(stream, X)
+    _check(lib().svdq_rope(plan.handle, code, T, H, D, positions.data_ptr(), R, ldp,
+                           X.data_ptr(), X.stride(0), X.stride(1), out.data_ptr(), out.stride(0),
+                           out.stride(1), 1 if inverse else 0, st), "svdq_rope")
+
+
 class SVDQLinear:
     """One packed layer plus the buffers of its two hot-path calls.
 
@@ -541,6 +827,110 @@ class NVFP4Linear(SVDQLinear):
     __call__ = forward
 
 
+class Linear16:
+    """A 16-bit linear layer (the layers that are not quantised): weight
+    [N, K] and bias [N], cuda bf16 or fp16, used in place.
+
+    forward(X) returns epi(X W^T + b) + residual on the current stream; with
+    save=True it keeps X and the pre-activation for backward(dY), which
+    returns (dX, dW, db).  Buffers are reallocated only when M changes, and
+    the next call reuses them.
+    """
+
+    def __init__(self, weight, bias=None, epilogue: int = EPI_NONE):
+        self.weight, self.bias, self.epilogue = weight, bias, epilogue
+        self._M = self._Mb = -1
+        self.Y = self.P = self._saved = None
+
+    @staticmethod
+    def _empty(rows, cols, like):
+        import torch                # rows of a multiple of 16 bytes
+        return torch.empty((rows, -(-cols // 8) * 8), dtype=like.dtype, device=like.device)[:, :cols]
+
+    def forward(self, X, residual=None, out=None, save: bool = False):
+        M, N = X.shape[0], self.weight.shape[0]
+        if M != self._M:
+            self.Y, self.P, self._M = self._empty(M, N, X), None, M
+        if save and self.epilogue != EPI_NONE and self.P is None:
+            self.P = self._empty(M, N, X)
+        Y = self.Y if out is None else out
+        keep = save and self.epilogue != EPI_NONE
+        svdq_linear16(X, self.weight, Y, self.bias, residual, self.epilogue,
+                      self.P if keep else None)
+        self._saved = X if save else None
+        return Y
+
+    def backward(self, dY):
+        import torch
+        if self._saved is None:
+            raise RuntimeError("backward needs a forward call with save=True")
+        X, W = self._saved, self.weight
+        M, (N, K) = X.shape[0], W.shape
+        if M != self._Mb:
+            n = svdq_linear16_backward_workspace(M, K, N, self.epilogue)
+            self.ws = torch.empty((n,), dtype=torch.uint8, device=X.device)
+            self.dX, self.dW = self._empty(M, K, X), self._empty(N, K, X)
+            self.db = None if self.bias is None else torch.empty_like(self.bias)
+            self._Mb = M
+        svdq_linear16_backward(dY, X, W, self.P if self.epilogue != EPI_NONE else None, self.dX,
+                               self.dW, self.db, self.ws, self.epilogue)
+        return self.dX, self.dW, self.db
+
+    __call__ = forward
+
+
+class LayerNorm:
+    """Layer norm with optional weight and bias ([K], or [groups, K] with
+    rows_per_group given to forward: the modulated norm), cuda tensors of the
+    input's type or fp32, used in place; weight_offset is added to weight.
+
+    forward(X) returns the norm on the current stream; with save=True it
+    keeps X and the statistics for backward(dY), which returns
+    (dX, dweight, dbias).  Buffers are reallocated only when X's shape or
+    type changes, and the next call reuses them.
+    """
+
+    def __init__(self, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0):
+        self.weight, self.bias, self.eps, self.weight_offset = weight, bias, eps, weight_offset
+        self._key = self._keyb = None
+        self.Y = self.mean = self.rstd = self._saved = None
+
+    def forward(self, X, out=None, rows_per_group: int = 0, save: bool = False):
+        import torch
+        M, K = X.shape
+        if (M, K, X.dtype) != self._key:
+            self.Y = Linear16._empty(M, K, X)
+            self.mean = torch.empty((M,), dtype=torch.float32, device=X.device)
+            self.rstd = torch.empty_like(self.mean)
+            self._key = (M, K, X.dtype)
+        Y = self.Y if out is None else out
+        svdq_layer_norm(X, Y, self.weight, self.bias, self.eps, self.weight_offset, rows_per_group,
+                        self.mean if save else None, self.rstd if save else None)
+        self._saved = (X, rows_per_group) if save else None
+        return Y
+
+    def backward(self, dY):
+        import torch
+        if self._saved is None:
+            raise RuntimeError("backward needs a forward call with save=True")
+        X, rpg = self._saved
+        M, K = X.shape
+        key = (M, K, X.dtype, rpg)
+        if key != self._keyb:
+            groups = -(-M // rpg) if rpg > 0 else 1
+            n = svdq_layer_norm_backward_workspace(M, K, rpg)
+            self.ws = torch.empty((n,), dtype=torch.uint8, device=X.device) if n else None
+            self.dX = Linear16._empty(M, K, X)
+            grad = lambda p: None if p is None else Linear16._empty(groups, K, p)
+            self.dw, self.db = grad(self.weight), grad(self.bias)
+            self._keyb = key
+        svdq_layer_norm_backward(dY, X, self.mean, self.rstd, self.dX, self.weight,
+                                 self.weight_offset, rpg, self.dw, self.db, self.ws)
+        return self.dX, self.dw, self.db
+
+    __call__ = forward
+
+
 class SVDQMLP:
     """Two packed layers applied in sequence, fc2(GELU(fc1(X))), as in a
     transformer block's feed-forward part.
@@ -551,11 +941,15 @@ class SVDQMLP:
     emitting fc2's codes, scales and Z), then svdq_linear(fc2): H never
     reaches device memory, and fc2's codes and scales are the same bits.
     Buffers are reallocated only when M changes.
+
+    norm: a LayerNorm in front of fc1 (its modulation groups are passed to
+    forward as rows_per_group), or None.
     """
 
-    def __init__(self, fc1: Weights, fc2: Weights):
+    def __init__(self, fc1: Weights, fc2: Weights, norm: LayerNorm | None = None):
         if fc2.K != fc1.N:
             raise ValueError("fc2's K must equal fc1's N")
+        self.norm = norm
         self.fc1 = SVDQLinear(fc1, EPI_GELU)
         self.fc2 = SVDQLinear(fc2)
         self._M = -1
@@ -572,10 +966,12 @@ class SVDQMLP:
             self._M = M
         return self.H, self.ws
 
-    def forward(self, X, fused: bool = False, out=None):
+    def forward(self, X, fused: bool = False, out=None, rows_per_group: int = 0):
         M = X.shape[0]
         H, ws = self.buffers(M, X.device)
         a, b = self.fc1, self.fc2
+        if self.norm is not None:
+            X = self.norm(X, rows_per_group=rows_per_group)
         Y = b.Y if out is None else out
         svdq_quantize_act(a.w, X, a.xq, a.s_x, a.Z)
         if fused:
@@ -584,6 +980,37 @@ class SVDQMLP:
             svdq_linear(a.w, a.xq, a.s_x, a.Z, H, EPI_GELU)
             svdq_quantize_act(b.w, H, b.xq, b.s_x, b.Z)
         svdq_linear(b.w, b.xq, b.s_x, b.Z, Y)
+        return Y
+
+    __call__ = forward
+
+
+class SVDQQKV:
+    """A packed QKV layer with the rotary positions of its queries and keys:
+    norm (a LayerNorm, or None), the W4A4 product, then svdq_rope in place on
+    the query and key heads of the product's rows.
+
+    The packed layer's N is (heads + 2 kv_heads) head_dim, its columns the
+    query heads, then the key heads, then the value heads; kv_heads defaults
+    to heads.
+    """
+
+    def __init__(self, weights: Weights, heads: int, head_dim: int, plan: RopePlan,
+                 norm: LayerNorm | None = None, kv_heads: int | None = None):
+        kv = heads if kv_heads is None else kv_heads
+        if weights.N != (heads + 2 * kv) * head_dim:
+            raise ValueError("N must equal (heads + 2 kv_heads) head_dim")
+        self.qkv = SVDQLinear(weights)
+        self.norm, self.plan = norm, plan
+        self.heads, self.kv_heads, self.head_dim = heads, kv, head_dim
+
+    def forward(self, X, positions, out=None, rows_per_group: int = 0):
+        """X bf16 [M, K], positions int32 [M or fewer, axes] -> bf16 [M, N]."""
+        if self.norm is not None:
+            X = self.norm(X, rows_per_group=rows_per_group)
+        Y = self.qkv(X, out)
+        qk = Y[:, :(self.heads + self.kv_heads) * self.head_dim].unflatten(1, (-1, self.head_dim))
+        svdq_rope(self.plan, positions, qk, qk)
         return Y
 
     __call__ = forward

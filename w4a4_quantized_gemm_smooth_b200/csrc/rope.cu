@@ -1,0 +1,250 @@
+// Rotary positions with several axes (svdq_rope): every pair of a head is
+// turned by position[axis] * frequency, shared by all heads of a token.
+//
+// The angle is formed modulo one turn without rounding: a frequency is held
+// as a 64-bit fraction of a turn, the low 64 bits of its product with the
+// 32-bit position are the angle's fraction of a turn, and their top 32 bits
+// (2^-32 turn) go through sincospi.  A far position thus costs no accuracy.
+//
+// Bound by memory: one read and one write of T H D elements.  A thread holds
+// the sines and cosines of one vector's pairs and walks the heads, so the
+// trigonometry is paid once per heads_per_thread heads.
+#include <cmath>
+#include <new>
+
+#include "elem.cuh"
+#include "ops16.h"
+
+struct svdq_rope_plan {
+  svdq::RopeTurns t;
+  int pairing;
+};
+
+namespace svdq {
+namespace {
+
+struct RopeArgs {
+  const int32_t* pos;
+  const void* x;
+  void* y;
+  long long ldxt, ldxh, ldyt, ldyh;
+  long long work;            // tokens * units
+  int pos_rows, ld_pos;
+  int heads, heads_per_thread;
+  int units;                 // vectors (interleaved) or rotating vector pairs + tail vectors (halves)
+  int pairs, rot_units;      // halves: the first rot_units units hold pairs
+  int inverse, in_place;
+};
+
+__device__ __forceinline__ void sincos_turn(int32_t pos, uint64_t turn, bool inverse, float& c,
+                                            float& s) {
+  const uint64_t a = (uint64_t)(int64_t)pos * turn;
+  const float half_turns = (float)(int32_t)(a >> 32) * 4.656612873077393e-10f;   // 2^-31
+  sincospif(half_turns, &s, &c);
+  if (inverse) s = -s;
+}
+
+constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_BATCH = 4;      // heads whose loads are in flight together
+
+// V elements per vector.  HALVES: a unit below rot_units holds pairs
+// [V unit, V unit + V) as two vectors P elements apart, a later unit one
+// vector past the pairs; interleaved: a unit is one vector.
+template <typename T, int V, int ALIGN>
+struct alignas(ALIGN) RopeVec {
+  T e[V];
+};
+
+template <typename T, int V, bool HALVES, int ALIGN>
+__global__ void __launch_bounds__(ROPE_THREADS)
+rope_kernel(const __grid_constant__ RopeTurns turns, const RopeArgs p) {
+  using VT = RopeVec<T, V, ALIGN>;
+  const long long i = (long long)blockIdx.x * ROPE_THREADS + threadIdx.x;
+  if (i >= p.work) return;
+  const long long tok = i / p.units;
+  const int u = (int)(i - tok * p.units);
+  const int h0 = blockIdx.y * p.heads_per_thread;
+  const int h1 = min(p.heads, h0 + p.heads_per_thread);
+  const T* x = static_cast<const T*>(p.x) + tok * p.ldxt;
+  T* y = static_cast<T*>(p.y) + tok * p.ldyt;
+  constexpr int NP = HALVES ? V : V / 2;          // pairs of a unit
+  const bool rot = HALVES ? u < p.rot_units : u * NP < p.pairs;
+  if (!rot) {
+    if (p.in_place) return;
+    const int d = HALVES ? 2 * p.pairs + (u - p.rot_units) * V : u * V;
+    for (int h = h0; h < h1; ++h)
+      *reinterpret_cast<VT*>(y + h * p.ldyh + d) = *reinterpret_cast<const VT*>(x + h * p.ldxh + d);
+    return;
+  }
+  const int32_t* pos = p.pos + (long long)(tok % p.pos_rows) * p.ld_pos;
+  float c[NP], s[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int pr = u * NP + j;
+    c[j] = 1.0f;
+    s[j] = 0.0f;
+    if (pr < p.pairs) sincos_turn(pos[turns.axis[pr]], turns.turn[pr], p.inverse != 0, c[j], s[j]);
+  }
+  const int d0 = u * V, d1 = d0 + p.pairs;
+  for (int h = h0; h < h1; h += ROPE_BATCH) {
+    VT a[ROPE_BATCH], b[ROPE_BATCH];
+#pragma unroll
+    for (int k = 0; k < ROPE_BATCH; ++k)
+      if (h + k < h1) {
+        a[k] = *reinterpret_cast<const VT*>(x + (h + k) * p.ldxh + d0);
+        if (HALVES) b[k] = *reinterpret_cast<const VT*>(x + (h + k) * p.ldxh + d1);
+      }
+#pragma unroll
+    for (int k = 0; k < ROPE_BATCH; ++k)
+      if (h + k < h1) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          T& ea = HALVES ? a[k].e[j] : a[k].e[2 * j];
+          T& eb = HALVES ? b[k].e[j] : a[k].e[2 * j + 1];
+          // a vector may straddle the last pair: what follows is copied as it is
+          if (HALVES || u * NP + j < p.pairs) {
+            const float fa = Elem<T>::to_f(ea), fb = Elem<T>::to_f(eb);
+            ea = Elem<T>::from_f(fa * c[j] - fb * s[j]);
+            eb = Elem<T>::from_f(fa * s[j] + fb * c[j]);
+          }
+        }
+        *reinterpret_cast<VT*>(y + (h + k) * p.ldyh + d0) = a[k];
+        if (HALVES) *reinterpret_cast<VT*>(y + (h + k) * p.ldyh + d1) = b[k];
+      }
+  }
+}
+
+template <typename T, int V, bool HALVES, int ALIGN = V * (int)sizeof(T)>
+cudaError_t launch_v(const RopeTurns& t, RopeArgs a, int tokens, int head_dim, cudaStream_t st) {
+  if (HALVES) {
+    a.rot_units = a.pairs / V;
+    a.units = a.rot_units + (head_dim - 2 * a.pairs) / V;
+  } else {
+    a.rot_units = 0;
+    a.units = head_dim / V;
+  }
+  a.work = (long long)tokens * a.units;
+  // Heads per thread: as many as 8 while the grid still covers the GPU with
+  // a thousand threads per SM; small batches spread the heads instead.
+  int hpt = 8;
+  while (hpt > 1 && a.work * ((a.heads + hpt - 1) / hpt) < 148 * 1024) hpt >>= 1;
+  a.heads_per_thread = hpt;
+  const long long blocks = (a.work + ROPE_THREADS - 1) / ROPE_THREADS;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + hpt - 1) / hpt));
+  rope_kernel<T, V, HALVES, ALIGN><<<grid, ROPE_THREADS, 0, st>>>(t, a);
+  return cudaGetLastError();
+}
+
+// The widest vector (up to 16 bytes) that every address is a multiple of.
+template <typename T>
+cudaError_t launch_t(const svdq_rope_plan* plan, const RopeArgs& a, int tokens, int head_dim,
+                     cudaStream_t st) {
+  constexpr int E = (int)sizeof(T);
+  const bool halves = plan->pairing == SVDQ_ROPE_HALVES;
+  uint64_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
+                  (uint64_t)(a.ldxt * E) | (uint64_t)(a.ldyt * E) | (uint64_t)(a.ldxh * E) |
+                  (uint64_t)(a.ldyh * E) | (uint64_t)head_dim * E;
+  if (halves) bits |= (uint64_t)a.pairs * E;
+  int v = 16 / E;
+  while (v > 1 && (bits & (uint64_t)(v * E - 1)) != 0) v >>= 1;
+  const RopeTurns& t = plan->t;
+  if (halves) {
+    if constexpr (E == 2)
+      if (v == 8) return launch_v<T, 8, true>(t, a, tokens, head_dim, st);
+    if (v == 4) return launch_v<T, 4, true>(t, a, tokens, head_dim, st);
+    if (v == 2) return launch_v<T, 2, true>(t, a, tokens, head_dim, st);
+    return launch_v<T, 1, true>(t, a, tokens, head_dim, st);
+  }
+  if constexpr (E == 2)
+    if (v == 8) return launch_v<T, 8, false>(t, a, tokens, head_dim, st);
+  if (v == 4) return launch_v<T, 4, false>(t, a, tokens, head_dim, st);
+  if (v == 2) return launch_v<T, 2, false>(t, a, tokens, head_dim, st);
+  return launch_v<T, 2, false, E>(t, a, tokens, head_dim, st);    // element by element
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const svdq_rope_plan* plan, int dtype, int tokens, int heads,
+                        int head_dim, const int32_t* pos, int pos_rows, int ld_pos, const void* X,
+                        long long ldxt, long long ldxh, void* Y, long long ldyt, long long ldyh,
+                        int inverse, cudaStream_t st) {
+  RopeArgs a{};
+  a.pos = pos; a.x = X; a.y = Y;
+  a.ldxt = ldxt; a.ldxh = ldxh; a.ldyt = ldyt; a.ldyh = ldyh;
+  a.pos_rows = pos_rows; a.ld_pos = ld_pos;
+  a.heads = heads; a.pairs = plan->t.pairs;
+  a.inverse = inverse; a.in_place = X == Y;
+  if (dtype == SVDQ_DTYPE_BF16) return launch_t<__nv_bfloat16>(plan, a, tokens, head_dim, st);
+  if (dtype == SVDQ_DTYPE_F16) return launch_t<__half>(plan, a, tokens, head_dim, st);
+  return launch_t<float>(plan, a, tokens, head_dim, st);
+}
+
+}  // namespace svdq
+
+extern "C" {
+
+svdq_status svdq_rope_create(int n_axes, const int* pairs_per_axis, const double* freq,
+                             int pairing, svdq_rope_plan** out) {
+  if (!out) return SVDQ_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!pairs_per_axis || !freq || n_axes < 1 || n_axes > SVDQ_ROPE_MAX_AXES ||
+      (pairing != SVDQ_ROPE_INTERLEAVED && pairing != SVDQ_ROPE_HALVES))
+    return SVDQ_ERR_INVALID_ARG;
+  int pairs = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (pairs_per_axis[a] < 0 || pairs_per_axis[a] > SVDQ_ROPE_MAX_PAIRS) return SVDQ_ERR_SHAPE;
+    pairs += pairs_per_axis[a];
+  }
+  if (pairs < 1 || pairs > SVDQ_ROPE_MAX_PAIRS) return SVDQ_ERR_SHAPE;
+  for (int p = 0; p < pairs; ++p)
+    if (!(std::fabs(freq[p]) < 1048576.0)) return SVDQ_ERR_NUMERIC;
+  svdq_rope_plan* plan = new (std::nothrow) svdq_rope_plan();
+  if (!plan) return SVDQ_ERR_OOM;
+  plan->pairing = pairing;
+  plan->t.pairs = pairs;
+  plan->t.axes = n_axes;
+  int p = 0;
+  for (int a = 0; a < n_axes; ++a)
+    for (int j = 0; j < pairs_per_axis[a]; ++j, ++p) {
+      plan->t.axis[p] = (uint8_t)a;
+      // fraction of a turn in [0, 1) times 2^64, in 64-bit-mantissa arithmetic
+      const long double two_pi = 6.283185307179586476925286766559005768L;
+      long double f = (long double)freq[p] / two_pi;
+      f -= floorl(f);
+      const long double scaled = floorl(ldexpl(f, 64) + 0.5L);
+      plan->t.turn[p] = scaled >= ldexpl(1.0L, 64) ? 0ull : (uint64_t)scaled;
+    }
+  *out = plan;
+  return SVDQ_OK;
+}
+
+void svdq_rope_free(svdq_rope_plan* plan) { delete plan; }
+
+svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int heads, int head_dim,
+                      const int32_t* positions, int pos_rows, int ld_pos, const void* X,
+                      long long ldx_token, long long ldx_head, void* Y, long long ldy_token,
+                      long long ldy_head, int inverse, cudaStream_t stream) {
+  if (!plan || dtype < SVDQ_DTYPE_BF16 || dtype > SVDQ_DTYPE_F32) return SVDQ_ERR_INVALID_ARG;
+  if (tokens < 0 || heads < 0 || pos_rows < 1 || ld_pos < plan->t.axes || head_dim < 2 ||
+      head_dim % 2 != 0 || head_dim < 2 * plan->t.pairs || ldx_token < 0 || ldx_head < 0 ||
+      ldy_token < 0 || ldy_head < 0)
+    return SVDQ_ERR_SHAPE;
+  if (head_dim > SVDQ_ROPE_MAX_HEAD_DIM || heads > SVDQ_ROPE_MAX_HEADS) return SVDQ_ERR_UNSUPPORTED;
+  if (tokens == 0 || heads == 0) return SVDQ_OK;
+  if (!positions || !X || !Y) return SVDQ_ERR_INVALID_ARG;
+  // two heads or tokens never share an element of Y
+  const long long hd = head_dim;
+  if ((heads > 1 && ldy_head < hd) || (tokens > 1 && ldy_token < hd)) return SVDQ_ERR_SHAPE;
+  if (X == Y && ((tokens > 1 && ldx_token != ldy_token) || (heads > 1 && ldx_head != ldy_head)))
+    return SVDQ_ERR_INVALID_ARG;
+  const uintptr_t e = dtype == SVDQ_DTYPE_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(X) & e) || (reinterpret_cast<uintptr_t>(Y) & e) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3))
+    return SVDQ_ERR_ALIGNMENT;
+  return svdq::launch_rope(plan, dtype, tokens, heads, head_dim, positions, pos_rows, ld_pos, X,
+                           ldx_token, ldx_head, Y, ldy_token, ldy_head, inverse,
+                           stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
+}  // extern "C"
