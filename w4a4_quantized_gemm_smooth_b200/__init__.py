@@ -486,61 +486,70 @@ def svdq_debug_partials(w: Weights, M, xq, row0, nrows, col0, ncols, P, stream=N
 # tensors, so the binding checks each one's device, type and shape before it
 # passes the pointer on (ValueError); the library checks sizes and alignment.
 
+# They are written for a short host path: a call costs a few microseconds.
+
+_torch = None
 _DTYPES: dict = {}
 
 
 def _dtype_code(t, name="X"):
-    if not _DTYPES:
+    global _torch
+    if _torch is None:
         import torch
         _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        _torch = torch
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: dtype {t.dtype} is not supported")
     return code
 
 
-def _raw_stream(stream, t):
-    """The stream's handle; None: the current stream of t's device, which has
-    to be the current device (launches go there)."""
-    import torch
-    dev = t.get_device()
+def _raw_stream(stream, dev):
+    """The stream's handle; None: the current stream of device `dev` (the
+    tensors' one), which has to be the current device: launches go there."""
     if dev < 0:
         raise ValueError("the tensors have to be on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != _torch.cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
 
 
-def _matrix(t, name, rows, cols, like):
-    """(pointer, leading dimension) of a [rows, cols] tensor on like's device,
-    of like's type."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+def _matrix(t, name, rows, cols, dtype, dev):
+    """(pointer, leading dimension) of a [rows, cols] tensor of type `dtype`
+    on device `dev` with contiguous rows."""
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    ld = t.stride(0)
-    if cols > 1 and t.stride(1) != 1:
+    if t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype} on cuda:{dev}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name}: rows have to be contiguous")
     if rows <= 1:
         ld = -(-cols // 8) * 8          # a single row has no pitch
     return t.data_ptr(), ld
 
 
-def _vector(t, name, n, like, dtype=None):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+def _opt_matrix(t, name, rows, cols, dtype, dev):
+    return (None, 0) if t is None else _matrix(t, name, rows, cols, dtype, dev)
+
+
+def _opt_vector(t, name, n, dtype, dev):
+    if t is None:
+        return None
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name}: expected {n} contiguous values")
-    if t.dtype != (dtype or like.dtype) or t.device != like.device:
-        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype or like.dtype} on {like.device}")
+    if t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _workspace(ws, like):
+def _opt_workspace(ws, dev):
     if ws is None:
         return None, 0
-    if ws.device != like.device or not ws.is_contiguous():
-        raise ValueError("workspace: expected a contiguous tensor on the operands' device")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -548,16 +557,16 @@ def svdq_linear16(X, W, Y, bias=None, residual=None, epilogue=EPI_NONE, preact=N
     """Y = epi(X W^T + bias) + residual.  X [M, K], W [N, K], Y [M, N], all
     cuda bf16 or fp16 with contiguous rows; bias [N]; residual [M, N] (may be
     Y); preact [M, N] receives X W^T + bias for svdq_linear16_backward."""
-    code = _dtype_code(X)
+    code, dev, dt = _dtype_code(X), X.get_device(), X.dtype
     M, K = X.shape
     N = W.shape[0]
-    st = _raw_stream(stream, X)
-    x, ldx = _matrix(X, "X", M, K, X)
-    w, ldw = _matrix(W, "W", N, K, X)
-    y, ldy = _matrix(Y, "Y", M, N, X)
-    b = None if bias is None else _vector(bias, "bias", N, X)
-    r, ldr = (None, 0) if residual is None else _matrix(residual, "residual", M, N, X)
-    p, ldp = (None, 0) if preact is None else _matrix(preact, "preact", M, N, X)
+    st = _raw_stream(stream, dev)
+    x, ldx = _matrix(X, "X", M, K, dt, dev)
+    w, ldw = _matrix(W, "W", N, K, dt, dev)
+    y, ldy = _matrix(Y, "Y", M, N, dt, dev)
+    b = _opt_vector(bias, "bias", N, dt, dev)
+    r, ldr = _opt_matrix(residual, "residual", M, N, dt, dev)
+    p, ldp = _opt_matrix(preact, "preact", M, N, dt, dev)
     _check(lib().svdq_linear16(code, M, K, N, x, ldx, w, ldw, b, r, ldr, epilogue, y, ldy, p, ldp,
                                st), "svdq_linear16")
 
@@ -572,19 +581,21 @@ def svdq_linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue=
     """Gradients of svdq_linear16: dX [M, K], dW [N, K] and dbias [N] (each may
     be None) for dY [M, N]; preact is the forward call's (None without an
     activation).  The residual's gradient is dY itself."""
-    code = _dtype_code(dY, "dY")
+    code, dev, dt = _dtype_code(dY, "dY"), dY.get_device(), dY.dtype
     M, N = dY.shape
-    K = X.shape[1] if X is not None else W.shape[1]
-    st = _raw_stream(stream, dY)
-    d, ldd = _matrix(dY, "dY", M, N, dY)
-    opt = lambda t, name, r, c: (None, 0) if t is None else _matrix(t, name, r, c, dY)
-    x, ldx = opt(X, "X", M, K)
-    w, ldw = opt(W, "W", N, K)
-    p, ldp = opt(preact, "preact", M, N)
-    gx, ldgx = opt(dX, "dX", M, K)
-    gw, ldgw = opt(dW, "dW", N, K)
-    gb = None if dbias is None else _vector(dbias, "dbias", N, dY)
-    ws, nbytes = _workspace(workspace, dY)
+    if X is None and W is None:
+        K = 1                       # only dbias is wanted
+    else:
+        K = (X if X is not None else W).shape[1]
+    st = _raw_stream(stream, dev)
+    d, ldd = _matrix(dY, "dY", M, N, dt, dev)
+    x, ldx = _opt_matrix(X, "X", M, K, dt, dev)
+    w, ldw = _opt_matrix(W, "W", N, K, dt, dev)
+    p, ldp = _opt_matrix(preact, "preact", M, N, dt, dev)
+    gx, ldgx = _opt_matrix(dX, "dX", M, K, dt, dev)
+    gw, ldgw = _opt_matrix(dW, "dW", N, K, dt, dev)
+    gb = _opt_vector(dbias, "dbias", N, dt, dev)
+    ws, nbytes = _opt_workspace(workspace, dev)
     _check(lib().svdq_linear16_backward(code, M, K, N, d, ldd, x, ldx, w, ldw, p, ldp, epilogue,
                                         gx, ldgx, gw, ldgw, gb, ws, nbytes, st),
            "svdq_linear16_backward")
@@ -596,29 +607,36 @@ def svdq_get_op_error(stream=None):
     _check(lib().svdq_get_op_error(_stream_ptr(stream)), "device")
 
 
-def _params(t, name, groups, K, like, shared=True):
+def _params(t, name, groups, K, dev, shared=True):
     """(pointer, leading dimension) of a parameter [groups, K] or [K] (shared
-    by every group) and its type's code."""
-    if t.device != like.device or t.shape[-1] != K or t.dim() not in (1, 2) or \
+    by every group); a gradient (not shared) has a row per group."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if t.get_device() != dev or len(shape) not in (1, 2) or shape[-1] != K or \
             (K > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name}: expected [{groups}, {K}] or [{K}] with contiguous rows on {like.device}")
-    if t.dim() == 1 or t.shape[0] == 1:
+        raise ValueError(f"{name}: expected [{groups}, {K}] or [{K}] with contiguous rows on cuda:{dev}")
+    if len(shape) == 1 or shape[0] == 1:
         if not shared and groups != 1:
             raise ValueError(f"{name}: expected [{groups}, {K}]")
         return t.data_ptr(), 0 if shared else -(-K // 8) * 8
-    if t.shape[0] != groups:
+    if shape[0] != groups:
         raise ValueError(f"{name}: expected {groups} rows")
     return t.data_ptr(), t.stride(0)
 
 
 def _param_code(X, *ps):
     """The parameters' common type code (X's type or float32)."""
-    ts = [p for p in ps if p is not None]
-    if not ts:
-        return _dtype_code(X)
-    if any(p.dtype != ts[0].dtype for p in ts):
-        raise ValueError("the parameters and their gradients have to be of one type")
-    return _dtype_code(ts[0], "parameter")
+    dt = None
+    for p in ps:
+        if p is not None:
+            if dt is not None and p.dtype != dt:
+                raise ValueError("the parameters and their gradients have to be of one type")
+            dt = p.dtype
+    code = _DTYPES.get(X.dtype if dt is None else dt)
+    if code is None:
+        raise ValueError(f"parameters: dtype {dt} is not supported")
+    return code
 
 
 def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, rows_per_group=0,
@@ -627,18 +645,17 @@ def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, r
     [M, K] (bf16, fp16 or fp32).  weight, bias: [K], or [groups, K] with one
     row for every rows_per_group rows of X; X's type or fp32.  mean, rstd:
     fp32 [M], the statistics for svdq_layer_norm_backward.  Y may be X."""
-    import torch
-    code = _dtype_code(X)
+    code, dev, dt = _dtype_code(X), X.get_device(), X.dtype
     M, K = X.shape
-    st = _raw_stream(stream, X)
-    x, ldx = _matrix(X, "X", M, K, X)
-    y, ldy = _matrix(Y, "Y", M, K, X)
+    st = _raw_stream(stream, dev)
+    x, ldx = _matrix(X, "X", M, K, dt, dev)
+    y, ldy = _matrix(Y, "Y", M, K, dt, dev)
     pc = _param_code(X, weight, bias)
     groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
-    w, ldw = (None, 0) if weight is None else _params(weight, "weight", groups, K, X)
-    b, ldb = (None, 0) if bias is None else _params(bias, "bias", groups, K, X)
-    mu = None if mean is None else _vector(mean, "mean", M, X, torch.float32)
-    rs = None if rstd is None else _vector(rstd, "rstd", M, X, torch.float32)
+    w, ldw = _params(weight, "weight", groups, K, dev)
+    b, ldb = _params(bias, "bias", groups, K, dev)
+    mu = _opt_vector(mean, "mean", M, _torch.float32, dev)
+    rs = _opt_vector(rstd, "rstd", M, _torch.float32, dev)
     _check(lib().svdq_layer_norm(code, pc, M, K, x, ldx, w, ldw, b, ldb, weight_offset,
                                  rows_per_group, eps, y, ldy, mu, rs, st), "svdq_layer_norm")
 
@@ -653,21 +670,20 @@ def svdq_layer_norm_backward(dY, X, mean, rstd, dX, weight=None, weight_offset=0
                              stream=None):
     """Gradients of svdq_layer_norm: dX [M, K] (may be dY or X), dweight and
     dbias [groups, K] or, with one group, [K]; each may be None."""
-    import torch
-    code = _dtype_code(X)
+    code, dev, dt = _dtype_code(X), X.get_device(), X.dtype
     M, K = X.shape
-    st = _raw_stream(stream, X)
-    d, ldd = _matrix(dY, "dY", M, K, X)
-    x, ldx = _matrix(X, "X", M, K, X)
-    gx, ldgx = (None, 0) if dX is None else _matrix(dX, "dX", M, K, X)
+    st = _raw_stream(stream, dev)
+    d, ldd = _matrix(dY, "dY", M, K, dt, dev)
+    x, ldx = _matrix(X, "X", M, K, dt, dev)
+    gx, ldgx = _opt_matrix(dX, "dX", M, K, dt, dev)
     pc = _param_code(X, weight, dweight, dbias)
     groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
-    w, ldw = (None, 0) if weight is None else _params(weight, "weight", groups, K, X)
-    gw, ldgw = (None, 0) if dweight is None else _params(dweight, "dweight", groups, K, X, False)
-    gb, ldgb = (None, 0) if dbias is None else _params(dbias, "dbias", groups, K, X, False)
-    mu = _vector(mean, "mean", M, X, torch.float32)
-    rs = _vector(rstd, "rstd", M, X, torch.float32)
-    ws, nbytes = _workspace(workspace, X)
+    w, ldw = _params(weight, "weight", groups, K, dev)
+    gw, ldgw = _params(dweight, "dweight", groups, K, dev, False)
+    gb, ldgb = _params(dbias, "dbias", groups, K, dev, False)
+    mu = _opt_vector(mean, "mean", M, _torch.float32, dev)
+    rs = _opt_vector(rstd, "rstd", M, _torch.float32, dev)
+    ws, nbytes = _opt_workspace(workspace, dev)
     _check(lib().svdq_layer_norm_backward(code, pc, M, K, d, ldd, x, ldx, mu, rs, w, ldw,
                                           weight_offset, rows_per_group, gx, ldgx, gw, ldgw, gb,
                                           ldgb, ws, nbytes, st), "svdq_layer_norm_backward")
@@ -719,23 +735,23 @@ def svdq_rope(plan: RopePlan, positions, X, out, inverse=False, stream=None):
     head strides) into out (same shape; X itself rotates in place).
     positions: int32 [T, axes], or [R, axes] shared by tokens t with equal
     t % R.  inverse: the opposite rotation, the gradient of the first."""
-    import torch
-    code = _dtype_code(X)
-    if X.dim() != 3 or out.shape != X.shape or out.dtype != X.dtype or out.device != X.device:
+    code, dev, shape = _dtype_code(X), X.get_device(), X.shape
+    if len(shape) != 3 or out.shape != shape or out.dtype != X.dtype or out.get_device() != dev:
         raise ValueError("X and out: expected [tokens, heads, head_dim] of one type and device")
-    T, H, D = X.shape
-    if D > 1 and (X.stride(2) != 1 or out.stride(2) != 1):
+    T, H, D = shape
+    xt, xh, x1 = X.stride()
+    yt, yh, y1 = out.stride()
+    if D > 1 and (x1 != 1 or y1 != 1):
         raise ValueError("X and out: a head's elements have to be contiguous")
-    if positions.dim() != 2 or positions.shape[1] != plan.n_axes or \
-            positions.dtype != torch.int32 or positions.device != X.device or \
-            (plan.n_axes > 1 and positions.stride(1) != 1):
-        raise ValueError(f"positions: expected int32 [rows, {plan.n_axes}] on {X.device}")
-    R = positions.shape[0]
-    ldp = positions.stride(0) if R > 1 else plan.n_axes
-    st = _raw_stream(stream, X)
-    _check(lib().svdq_rope(plan.handle, code, T, H, D, positions.data_ptr(), R, ldp,
-                           X.data_ptr(), X.stride(0), X.stride(1), out.data_ptr(), out.stride(0),
-                           out.stride(1), 1 if inverse else 0, st), "svdq_rope")
+    axes, pshape = plan.n_axes, positions.shape
+    if len(pshape) != 2 or pshape[1] != axes or positions.dtype != _torch.int32 or \
+            positions.get_device() != dev or (axes > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions: expected int32 [rows, {axes}] on cuda:{dev}")
+    R = pshape[0]
+    ldp = positions.stride(0) if R > 1 else axes
+    st = _raw_stream(stream, dev)
+    _check(lib().svdq_rope(plan._h, code, T, H, D, positions.data_ptr(), R, ldp, X.data_ptr(), xt,
+                           xh, out.data_ptr(), yt, yh, 1 if inverse else 0, st), "svdq_rope")
 
 
 class SVDQLinear:

@@ -11,6 +11,7 @@ only when a source or header is newer.
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import glob
 import os
 import shutil
@@ -50,7 +51,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     headers = (glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
                glob.glob(os.path.join(INCLUDE, "*.h")))
     hdr_time = _newest(headers) if headers else 0.0
-    objs = []
+    objs, jobs = [], []
     for src in sources:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         objs.append(obj)
@@ -60,14 +61,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc, *ARCH, *COMMON, "-c", src, "-o", obj]
         if src.endswith(".cu") and verbose:
             cmd += ["-Xptxas", "-v"]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if verbose or res.returncode != 0:
-            sys.stdout.write(res.stdout)
-            sys.stderr.write(res.stderr)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+        jobs.append((src, cmd))
+
+    def compile_one(job):
+        return job, subprocess.run(job[1], capture_output=True, text=True)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        for (src, cmd), res in pool.map(compile_one, jobs):
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            if verbose or res.returncode != 0:
+                sys.stdout.write(res.stdout)
+                sys.stderr.write(res.stderr)
+            if res.returncode != 0:
+                raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-Xcompiler", "-fopenmp",
                "-lcudart", "-lgomp"]

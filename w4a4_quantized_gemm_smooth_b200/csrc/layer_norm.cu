@@ -1,20 +1,27 @@
 // Layer norm with a scale and a shift per group of rows, and its gradients.
 //
-// Forward: a row is held in the registers of one team (a warp, or a block of
-// 128 or 512 threads for long rows), so that X is read once although the
-// variance is the two-pass one, sum (x - mu)^2 in fp32 after the mean (no
-// cancellation for rows with a large mean).  Bound by memory.
+// A row belongs to one team (a warp, or a block of 128 or 512 threads for
+// long rows), and a team walks over rows of one group.  Each thread copies
+// its own 16-byte vectors of the next rows to its own places in shared
+// memory (cp.async, no barrier), so that the bytes in flight do not depend
+// on the registers that a row needs; the scale and the shift wait there too.
+// Arithmetic runs on pairs (packed fp32 instructions), which keeps it below
+// the memory time.
 //
-// Backward: a team owns fixed columns and walks over rows of one group.  Per
-// row it forms the two row sums and dX from registers; the columns' sums of
-// dy xhat and dy stay in registers over all the rows of the team and are
-// joined at the end: teams of a block in shared memory in order, blocks of a
-// group through fp32 partials in the workspace, summed in block order by a
-// second kernel.  X and dY are read once.
+// Forward: the variance is the two-pass one, sum (x - mu)^2 in fp32 after the
+// mean, from registers (no cancellation for rows with a large mean).
+//
+// Backward: a thread owns fixed columns; their sums of dy xhat and dy stay in
+// its registers over all the rows of the team and are joined at the end:
+// teams of a block in shared memory in order, blocks of a group through fp32
+// partials in the workspace, summed in block order by a second kernel.  X and
+// dY are read once.
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
 #include "elem.cuh"
+#include "gemm_common.cuh"
 #include "ops16.h"
 
 namespace svdq {
@@ -28,12 +35,104 @@ struct NormArgs {
   float* mean;
   float* rstd;
   long long ldx, ldw, ldb, ldy;
-  int M, K, rows_per_group;
+  int M, K, rows_per_group;  // rows_per_group >= 1 here
+  int splits;                // blocks per group
   float w0, eps;
 };
 
+// The rows of a group that a block walks over.
+struct RowSpan {
+  long long g, r0, r1;
+};
+__device__ __forceinline__ RowSpan block_span(int M, int rows_per_group, int splits) {
+  RowSpan s;
+  s.g = blockIdx.x / (unsigned)splits;
+  const int k = (int)(blockIdx.x - (unsigned)s.g * splits);
+  const long long g0 = s.g * rows_per_group;
+  const long long len = min((long long)rows_per_group, M - g0);
+  s.r0 = g0 + len * k / splits;
+  s.r1 = g0 + len * (k + 1) / splits;
+  return s;
+}
+
+// How a row of up to G NV V elements (V = 16 / sizeof(T)) is held: threads of
+// a block, teams of a block, rows in flight per team, and whether the scale
+// and shift are kept in shared memory (not for the longest rows, which need
+// the room; they are read from the caches).
+template <typename T, int G, int NV>
+struct NormCfg {
+  static constexpr int V = 16 / (int)sizeof(T), H = V / 2;
+  static constexpr int THREADS = G > 128 ? G : 128;
+  static constexpr int TEAMS = THREADS / G;
+  static constexpr bool PSMEM = G < 512;
+  static constexpr int DF = G < 512 ? 3 : 2;                   // rows in flight, forward
+  static constexpr int DB = NV < 8 ? 2 : 1;                    // backward (x and dy)
+  static constexpr size_t PARAM = PSMEM ? (size_t)NV * G * V * 4 : 0;   // one fp32 row
+  static constexpr size_t RING_FWD = (size_t)DF * NV * THREADS * 16;
+  static constexpr size_t RING_BWD = (size_t)DB * 2 * NV * THREADS * 16;
+  static constexpr size_t FWD_SMEM = RING_FWD + 2 * PARAM;
+  static constexpr size_t BWD_SMEM = RING_BWD + PARAM;
+  static_assert(FWD_SMEM <= 227 * 1024 && BWD_SMEM <= 227 * 1024, "shared memory");
+  static_assert(TEAMS == 1 || (size_t)2 * NV * G * V * 4 <= RING_BWD, "column sums fit the ring");
+};
+
+// A thread's share of a row: vectors at elements c(i) = (lane + i G) V, and
+// how many bytes of the last one lie in the row of K elements (the others
+// lie in it whole).
+template <typename T, int G, int NV>
+struct RowShare {
+  static constexpr int V = 16 / (int)sizeof(T);
+  int last;
+  __device__ __forceinline__ RowShare(int lane, int K) {
+    const int left = (K - (lane + (NV - 1) * G) * V) * (int)sizeof(T);
+    last = left < 0 ? 0 : left < 16 ? left : 16;
+  }
+  // Asynchronous copy of the share to dst, dst + pitch, ...; zeros past the row.
+  __device__ __forceinline__ void fetch(const T* row, int lane, uint32_t dst, uint32_t pitch) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const T* src = row + (i + 1 < NV || last ? (lane + i * G) * V : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                   ::"r"(dst + i * pitch), "l"(src), "r"(i + 1 < NV ? 16 : last) : "memory");
+    }
+  }
+};
+
+// A parameter row as fp32 in shared memory: float4 k of a thread's vector i
+// at (i V / 4 + k) G + lane, so that a warp reads consecutive float4s.
+template <typename PT, int V, int G, int NV>
+__device__ __forceinline__ void stage_param(float4* dst, const PT* row, int K, int lane, float add) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const RowVec<PT, V> q = load_vec<PT, V>(row, (lane + i * G) * V, K);
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      const float2 a = q.get(2 * k), b = q.get(2 * k + 1);
+      dst[(i * (V / 4) + k) * G + lane] = make_float4(a.x + add, a.y + add, b.x + add, b.y + add);
+    }
+  }
+}
+// Pairs of a thread's vector i: from shared memory, or from the row itself.
+template <typename PT, int V, int G, bool SMEM>
+__device__ __forceinline__ void read_param(float2 (&out)[V / 2], const float4* staged, const PT* row,
+                                           int K, int lane, int i, float add) {
+  if constexpr (SMEM) {
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      const float4 f = staged[(i * (V / 4) + k) * G + lane];
+      out[2 * k] = make_float2(f.x, f.y);
+      out[2 * k + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+    const RowVec<PT, V> q = load_vec<PT, V>(row, (lane + i * G) * V, K);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) out[j] = __fadd2_rn(q.get(j), splat2(add));
+  }
+}
+
 // Sum over a team of G threads (G = 32: the warp; else the whole block).
-// `red` has room for 2 x G / 32 values; two calls in a row use `phase` 0 and 1.
+// `red` has room for G / 32 values per phase; successive calls alternate
+// between two phases, so that one barrier per call is enough.
 template <int G>
 __device__ __forceinline__ float team_sum(float v, float* red, int phase) {
   v = warp_sum(v);
@@ -49,83 +148,118 @@ __device__ __forceinline__ float team_sum(float v, float* red, int phase) {
   return v;
 }
 
-// V elements per vector (16 bytes of T), NV vectors per thread.
-template <typename T, typename PT, int G, int NV>
-__global__ void __launch_bounds__(G > 128 ? G : 128)
-norm_kernel(const NormArgs p) {
-  constexpr int V = 16 / (int)sizeof(T);
-  constexpr int TEAMS = G >= 128 ? 1 : 128 / G;
-  __shared__ float red[2 * (G > 32 ? G / 32 : 1)];
-  const int lane = threadIdx.x % G;
-  const long long row = (long long)blockIdx.x * TEAMS + threadIdx.x / G;
-  if (row >= p.M) return;                 // whole teams only
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  float v[NV][V];
-  float sum = 0.0f;
+template <int H>
+__device__ __forceinline__ float sum_pairs(const float2 (&a)[H]) {
+  float2 s = a[0];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * G) * V;
-    if (c < p.K) {
-      load_row<T, V>(x, c, p.K, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] = 0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) sum += v[i][e];
-  }
-  const float inv_k = 1.0f / (float)p.K;
-  const float mu = team_sum<G>(sum, red, 0) * inv_k;
-  float sq = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * G) * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float d = v[i][e] - mu;
-      if (c + e < p.K) sq += d * d;
-    }
-  }
-  const float rstd = 1.0f / sqrtf(team_sum<G>(sq, red, 1) * inv_k + p.eps);
-  if (lane == 0) {
-    if (p.mean) p.mean[row] = mu;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
-  const long long g = p.rows_per_group ? row / p.rows_per_group : 0;
-  const PT* w = p.w ? static_cast<const PT*>(p.w) + g * p.ldw : nullptr;
-  const PT* b = p.b ? static_cast<const PT*>(p.b) + g * p.ldb : nullptr;
-  T* y = static_cast<T*>(p.y) + row * p.ldy;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (lane + i * G) * V;
-    if (c >= p.K) break;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[i][e] = (v[i][e] - mu) * rstd;
-    if (w) {
-      float t[V];
-      load_row<PT, V>(w, c, p.K, t);
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] *= t[e] + p.w0;
-    }
-    if (b) {
-      float t[V];
-      load_row<PT, V>(b, c, p.K, t);
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] += t[e];
-    }
-    store_row<T, V>(y, c, p.K, v[i]);
-  }
+  for (int j = 1; j < H; ++j) s = __fadd2_rn(s, a[j]);
+  return s.x + s.y;
 }
 
-// 16 bytes of a row from element c on; zeros past n.
-template <typename T>
-__device__ __forceinline__ Pack<T, 16> load_pack(const T* row, int c, int n) {
-  constexpr int V = 16 / (int)sizeof(T);
-  if (c + V <= n) return *reinterpret_cast<const Pack<T, 16>*>(row + c);
-  Pack<T, 16> v;
+template <typename T, typename PT, int G, int NV>
+__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 5 : 1)
+norm_kernel(const NormArgs p) {
+  using C = NormCfg<T, G, NV>;
+  constexpr int V = C::V, H = C::H, D = C::DF, TH = C::THREADS;
+  extern __shared__ uint4 smem[];
+  __shared__ float red[2 * (G > 32 ? G / 32 : 1)];
+  const int lane = threadIdx.x % G, team = threadIdx.x / G;
+  const RowSpan span = block_span(p.M, p.rows_per_group, p.splits);
+  const T* x = static_cast<const T*>(p.x);
+  const uint4* ring = smem + threadIdx.x;              // vector (slot, i) at (slot NV + i) TH
+  const uint32_t ring_u = smem_u32(ring);
+  float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_FWD);
+  float4* pb = pw + C::PARAM / 16;
+  const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
+  const PT* b = p.b ? static_cast<const PT*>(p.b) + span.g * p.ldb : nullptr;
+  const RowShare<T, G, NV> share(lane, p.K);
+  auto fetch = [&](long long row, int slot) {
+    if (row < span.r1) share.fetch(x + row * p.ldx, lane, ring_u + slot * NV * TH * 16, TH * 16);
+    cp_async_commit();
+  };
 #pragma unroll
-  for (int e = 0; e < V; ++e) v.e[e] = c + e < n ? row[c + e] : Elem<T>::from_f(0.0f);
-  return v;
+  for (int d = 0; d < D; ++d) fetch(span.r0 + team + d * C::TEAMS, d);
+  if constexpr (C::PSMEM) {
+    if (team == 0) {
+      if (w) stage_param<PT, V, G, NV>(pw, w, p.K, lane, p.w0);
+      if (b) stage_param<PT, V, G, NV>(pb, b, p.K, lane, 0.0f);
+    }
+    if (C::TEAMS > 1) __syncthreads();
+  }
+  const float inv_k = 1.0f / (float)p.K;
+  const bool ragged = p.K % V != 0;
+  int slot = 0;
+  for (long long row = span.r0 + team; row < span.r1; row += C::TEAMS) {
+    cp_async_wait<D - 1>();
+    float2 v[NV][H];
+    float2 acc[H];                        // independent sums, short chains
+#pragma unroll
+    for (int j = 0; j < H; ++j) acc[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const RowVec<T, V> q = read_vec<T, V>(ring + (slot * NV + i) * TH, TH);
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        v[i][j] = q.get(j);
+        acc[j] = __fadd2_rn(acc[j], v[i][j]);
+      }
+    }
+    const float mu = team_sum<G>(sum_pairs(acc), red, 0) * inv_k;
+    // every value of the slot is in registers: the row D further on may land there
+    fetch(row + (long long)D * C::TEAMS, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+    for (int j = 0; j < H; ++j) acc[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * G) * V;
+      const float2 m = splat2(i + 1 < NV || c < p.K ? -mu : 0.0f);   // what lies past the row stays 0
+#pragma unroll
+      for (int j = 0; j < H; ++j) v[i][j] = __fadd2_rn(v[i][j], m);
+      if (i + 1 == NV && ragged && c + V > p.K) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          if (c + 2 * j >= p.K) v[i][j].x = 0.0f;
+          if (c + 2 * j + 1 >= p.K) v[i][j].y = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) acc[j] = __ffma2_rn(v[i][j], v[i][j], acc[j]);
+    }
+    const float rstd = 1.0f / sqrtf(team_sum<G>(sum_pairs(acc), red, 1) * inv_k + p.eps);
+    if (lane == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    T* y = static_cast<T*>(p.y) + row * p.ldy;
+    const float2 r2 = splat2(rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * G) * V;
+      if (i + 1 < NV || c < p.K) {
+        RowVec<T, V> o;
+        float2 t[H], f[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) t[j] = r2;
+        if (w) {
+          read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
+#pragma unroll
+          for (int j = 0; j < H; ++j) t[j] = __fmul2_rn(r2, f[j]);
+        }
+        if (b) {
+          read_param<PT, V, G, C::PSMEM>(f, pb, b, p.K, lane, i, 0.0f);
+#pragma unroll
+          for (int j = 0; j < H; ++j) t[j] = __ffma2_rn(v[i][j], t[j], f[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < H; ++j) t[j] = __fmul2_rn(v[i][j], t[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) o.set(j, t[j]);
+        store_vec<T, V>(y, c, i + 1 < NV ? INT_MAX : p.K, o);
+      }
+    }
+  }
 }
 
 struct NormBwdArgs {
@@ -137,7 +271,7 @@ struct NormBwdArgs {
   void* dx;
   void* dw;
   void* db;
-  float* part;               // [items][2][K] when split, unused otherwise
+  float* part;               // [blocks][2][K] when split, unused otherwise
   long long lddy, ldx, ldw, lddx, lddw, lddb;
   int M, K, rows_per_group;  // rows_per_group >= 1 here
   int splits;                // blocks per group
@@ -146,115 +280,151 @@ struct NormBwdArgs {
 
 // PARAMS: dweight or dbias is wanted.
 template <typename T, typename PT, int G, int NV, bool PARAMS>
-__global__ void __launch_bounds__(G > 128 ? G : 128)
+__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 3 : 1)
 norm_bwd_kernel(const NormBwdArgs p) {
-  constexpr int V = 16 / (int)sizeof(T);
-  constexpr int TEAMS = G >= 128 ? 1 : 128 / G;
+  using C = NormCfg<T, G, NV>;
+  constexpr int V = C::V, H = C::H, D = C::DB, TH = C::THREADS, TEAMS = C::TEAMS;
+  extern __shared__ uint4 smem[];
   __shared__ float red[2 * (G > 32 ? 2 * (G / 32) : 1)];
-  extern __shared__ float colsum[];       // TEAMS > 1: [2][NV * G * V]
   const int lane = threadIdx.x % G, team = threadIdx.x / G;
-  const long long g = blockIdx.x / p.splits;
-  const int s = (int)(blockIdx.x - g * p.splits);
-  const long long g0 = g * p.rows_per_group;
-  const long long glen = min((long long)p.rows_per_group, p.M - g0);
-  const long long r0 = g0 + glen * s / p.splits, r1 = g0 + glen * (s + 1) / p.splits;
-  const PT* w = p.w ? static_cast<const PT*>(p.w) + g * p.ldw : nullptr;
+  const RowSpan span = block_span(p.M, p.rows_per_group, p.splits);
+  const T* x = static_cast<const T*>(p.x);
+  const T* dy = static_cast<const T*>(p.dy);
+  const uint4* ring = smem + threadIdx.x;    // slot: NV vectors of x, then NV of dy
+  const uint32_t ring_u = smem_u32(ring);
+  float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_BWD);
+  const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
+  const RowShare<T, G, NV> share(lane, p.K);
+  float nmu[D], nrs[D];                      // the statistics of the rows in flight
+  auto fetch = [&](long long row, int slot) {
+    if (row < span.r1) {
+      share.fetch(x + row * p.ldx, lane, ring_u + slot * 2 * NV * TH * 16, TH * 16);
+      share.fetch(dy + row * p.lddy, lane, ring_u + (slot * 2 + 1) * NV * TH * 16, TH * 16);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    const long long row = span.r0 + team + d * TEAMS;
+    fetch(row, d);
+    nmu[d] = row < span.r1 ? p.mean[row] : 0.0f;
+    nrs[d] = row < span.r1 ? p.rstd[row] : 0.0f;
+  }
   const float inv_k = 1.0f / (float)p.K;
-  float aw[PARAMS ? NV : 1][V], ab[PARAMS ? NV : 1][V];
+  float2 aw[PARAMS ? NV : 1][H], ab[PARAMS ? NV : 1][H];
   if constexpr (PARAMS) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e) aw[i][e] = ab[i][e] = 0.0f;
+      for (int j = 0; j < H; ++j) aw[i][j] = ab[i][j] = make_float2(0.0f, 0.0f);
   }
-  int phase = 0;
-  for (long long row = r0 + team; row < r1; row += TEAMS) {
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    const float mu = p.mean[row], rstd = p.rstd[row];
-    // the row stays packed in registers: the columns' sums need the room
-    Pack<T, 16> xr[NV], dr[NV];
+  if constexpr (C::PSMEM) {
+    if (w && team == 0) stage_param<PT, V, G, NV>(pw, w, p.K, lane, p.w0);
+    if (TEAMS > 1) __syncthreads();
+  }
+  int slot = 0, phase = 0;
+  for (long long row = span.r0 + team; row < span.r1; row += TEAMS) {
+    cp_async_wait<D - 1>();
+    const uint4* q = ring + slot * 2 * NV * TH;
+    const float2 m = splat2(-nmu[0]), r = splat2(nrs[0]);
+    // the statistics of the row D further on, long before they are needed
+    const long long ahead = row + (long long)D * TEAMS;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      xr[i] = load_pack(x, c, p.K);
-      dr[i] = load_pack(dy, c, p.K);
+    for (int d = 0; d + 1 < D; ++d) {
+      nmu[d] = nmu[d + 1];
+      nrs[d] = nrs[d + 1];
     }
-    float s1 = 0.0f, s2 = 0.0f;
+    if (ahead < span.r1) {
+      nmu[D - 1] = p.mean[ahead];
+      nrs[D - 1] = p.rstd[ahead];
+    }
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+    // columns past K: x and dy read as 0 and add 0 to every sum
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      float wv[V];
-      if (w && c < p.K) load_row<PT, V>(w, c, p.K, wv);
+      const RowVec<T, V> xr = read_vec<T, V>(q + i * TH, TH), dr = read_vec<T, V>(q + (NV + i) * TH, TH);
+      float2 f[H];
+      if (w) read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float dv = Elem<T>::to_f(dr[i].e[e]);
-        // columns past K: dy is 0, and xhat is set to 0
-        const float h = c + e < p.K ? (Elem<T>::to_f(xr[i].e[e]) - mu) * rstd : 0.0f;
+      for (int j = 0; j < H; ++j) {
+        const float2 d = dr.get(j);
+        const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m), r);
         if constexpr (PARAMS) {
-          aw[i][e] += dv * h;
-          ab[i][e] += dv;
+          aw[i][j] = __ffma2_rn(d, h, aw[i][j]);
+          ab[i][j] = __fadd2_rn(ab[i][j], d);
         }
-        const float t = w ? (c + e < p.K ? dv * (wv[e] + p.w0) : 0.0f) : dv;
-        s1 += t;
-        s2 += t * h;
+        const float2 t = w ? __fmul2_rn(d, f[j]) : d;
+        s1 = __fadd2_rn(s1, t);
+        s2 = __ffma2_rn(t, h, s2);
       }
     }
-    if (!p.dx) continue;
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (G > 32) {
-      constexpr int W = G / 32;
-      float* r = red + phase * 2 * W;     // two buffers: one barrier per row
-      if ((threadIdx.x & 31) == 0) {
-        r[threadIdx.x >> 5] = s1;
-        r[W + (threadIdx.x >> 5)] = s2;
-      }
-      __syncthreads();
-      s1 = s2 = 0.0f;
+    if (p.dx) {
+      float a1 = warp_sum(s1.x + s1.y), a2 = warp_sum(s2.x + s2.y);
+      if constexpr (G > 32) {
+        constexpr int W = G / 32;
+        float* rd = red + phase * 2 * W;    // two buffers: one barrier per row
+        if ((threadIdx.x & 31) == 0) {
+          rd[threadIdx.x >> 5] = a1;
+          rd[W + (threadIdx.x >> 5)] = a2;
+        }
+        __syncthreads();
+        a1 = a2 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        s1 += r[i];
-        s2 += r[W + i];
+        for (int i = 0; i < W; ++i) {
+          a1 += rd[i];
+          a2 += rd[W + i];
+        }
+        phase ^= 1;
       }
-      phase ^= 1;
+      // read the row again rather than hold it: its registers would halve the
+      // blocks on an SM
+      asm volatile("" ::: "memory");
+      const float2 n1 = splat2(-a1 * inv_k), n2 = splat2(-a2 * inv_k);
+      T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * G) * V;
+        if (i + 1 < NV || c < p.K) {
+          const RowVec<T, V> xr = read_vec<T, V>(q + i * TH, TH), dr = read_vec<T, V>(q + (NV + i) * TH, TH);
+          float2 f[H];
+          if (w) read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
+          RowVec<T, V> o;
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            const float2 d = dr.get(j);
+            const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m), r);
+            const float2 t = w ? __fmul2_rn(d, f[j]) : d;
+            o.set(j, __fmul2_rn(r, __ffma2_rn(h, n2, __fadd2_rn(t, n1))));
+          }
+          store_vec<T, V>(dx, c, i + 1 < NV ? INT_MAX : p.K, o);
+        }
+      }
     }
-    s1 *= inv_k;
-    s2 *= inv_k;
-    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      if (c >= p.K) break;
-      float wv[V], o[V];
-      if (w) load_row<PT, V>(w, c, p.K, wv);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float dv = Elem<T>::to_f(dr[i].e[e]);
-        const float h = (Elem<T>::to_f(xr[i].e[e]) - mu) * rstd;
-        o[e] = rstd * ((w ? dv * (wv[e] + p.w0) : dv) - s1 - h * s2);
-      }
-      store_row<T, V>(dx, c, p.K, o);
-    }
+    fetch(ahead, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
   }
   if constexpr (PARAMS) {
     if constexpr (TEAMS > 1) {
-      // join the teams in order
+      // join the teams in order, where the rows were (none is in flight)
       constexpr int COLS = NV * G * V;
+      float2* cw = reinterpret_cast<float2*>(smem);
+      float2* cb = cw + COLS / 2;
+      cp_async_wait<0>();
+      __syncthreads();
       for (int k = 0; k < TEAMS; ++k) {
         if (team == k) {
 #pragma unroll
           for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const int c = (lane + i * G) * V + e;
+            for (int j = 0; j < H; ++j) {
+              const int c = (lane + i * G) * H + j;
               if (k > 0) {
-                aw[i][e] += colsum[c];
-                ab[i][e] += colsum[COLS + c];
+                aw[i][j] = __fadd2_rn(cw[c], aw[i][j]);
+                ab[i][j] = __fadd2_rn(cb[c], ab[i][j]);
               }
               if (k < TEAMS - 1) {
-                colsum[c] = aw[i][e];
-                colsum[COLS + c] = ab[i][e];
+                cw[c] = aw[i][j];
+                cb[c] = ab[i][j];
               }
             }
         }
@@ -262,28 +432,37 @@ norm_bwd_kernel(const NormBwdArgs p) {
       }
       if (team != TEAMS - 1) return;
     }
-    if (p.splits == 1) {
-      PT* dw = p.dw ? static_cast<PT*>(p.dw) + g * p.lddw : nullptr;
-      PT* db = p.db ? static_cast<PT*>(p.db) + g * p.lddb : nullptr;
+    const bool whole = p.splits == 1;
+    // an own row of the gradients, or this block's partial row
+    PT* dw = whole && p.dw ? static_cast<PT*>(p.dw) + span.g * p.lddw : nullptr;
+    PT* db = whole && p.db ? static_cast<PT*>(p.db) + span.g * p.lddb : nullptr;
+    float* part = p.part + (whole ? 0 : (size_t)blockIdx.x * 2 * p.K);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (lane + i * G) * V;
-        if (c >= p.K) break;
-        if (dw) store_row<PT, V>(dw, c, p.K, aw[i]);
-        if (db) store_row<PT, V>(db, c, p.K, ab[i]);
-      }
-    } else {
-      float* pw = p.part + (size_t)blockIdx.x * 2 * p.K;
+    for (int i = 0; i < NV; ++i) {
+      const int c = (lane + i * G) * V;
+      if (c >= p.K) continue;
+      if (whole) {
+        RowVec<PT, V> ow, ob;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+        for (int j = 0; j < H; ++j) {
+          ow.set(j, aw[i][j]);
+          ob.set(j, ab[i][j]);
+        }
+        if (dw) store_vec<PT, V>(dw, c, p.K, ow);
+        if (db) store_vec<PT, V>(db, c, p.K, ob);
+      } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int c = (lane + i * G) * V + e;
-          if (c < p.K) {
-            pw[c] = aw[i][e];
-            pw[p.K + c] = ab[i][e];
+        for (int j = 0; j < H; ++j) {
+          if (c + 2 * j < p.K) {
+            part[c + 2 * j] = aw[i][j].x;
+            part[p.K + c + 2 * j] = ab[i][j].x;
+          }
+          if (c + 2 * j + 1 < p.K) {
+            part[c + 2 * j + 1] = aw[i][j].y;
+            part[p.K + c + 2 * j + 1] = ab[i][j].y;
           }
         }
+      }
     }
   }
 }
@@ -317,40 +496,67 @@ norm_bwd_join_kernel(const float* part, int splits, int K, PT* dw, long long ldd
   }
 }
 
-// Blocks per group of the backward pass: about four per SM over all groups,
-// with at least eight rows per block (two per warp of a four-warp block), so
-// that the partials stay a small share of the traffic.
-int bwd_splits(int M, int rows_per_group) {
+// Blocks per group: `per_sm` blocks per SM over all groups (what fits there
+// at once), with at least `rows` rows each.
+int split_rows(int M, int rows_per_group, int per_sm, int rows) {
   const long long groups = ((long long)M + rows_per_group - 1) / rows_per_group;
   const long long len = rows_per_group < M ? rows_per_group : M;
-  long long s = (4 * 148 + groups - 1) / groups;
-  const long long most = (len + 7) / 8;
+  long long s = (long long)per_sm * 148 / groups;
+  const long long most = (len + rows - 1) / rows;
   if (s > most) s = most;
   return (int)(s < 1 ? 1 : s);
 }
+// Backward: at least eight rows per block (two per warp of a four-warp
+// block), so that the partial sums stay a small share of the traffic.
+int bwd_splits(int M, int rows_per_group) { return split_rows(M, rows_per_group, 3, 8); }
+
+// Raises the kernel's dynamic shared-memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, bool* done) {
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
 
 template <typename T, typename PT, int G, int NV>
-cudaError_t fwd_launch(const NormArgs& a, cudaStream_t st) {
-  constexpr int TEAMS = G >= 128 ? 1 : 128 / G;
-  const long long blocks = ((long long)a.M + TEAMS - 1) / TEAMS;
-  norm_kernel<T, PT, G, NV><<<(unsigned)blocks, G > 128 ? G : 128, 0, st>>>(a);
+cudaError_t fwd_launch(NormArgs a, cudaStream_t st) {
+  using C = NormCfg<T, G, NV>;
+  static bool done[kMaxDevices] = {};
+  const cudaError_t e = allow_smem(norm_kernel<T, PT, G, NV>, C::FWD_SMEM, done);
+  if (e != cudaSuccess) return e;
+  const long long groups = ((long long)a.M + a.rows_per_group - 1) / a.rows_per_group;
+  a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : 5, C::TEAMS);
+  norm_kernel<T, PT, G, NV><<<(unsigned)(groups * a.splits), C::THREADS, C::FWD_SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
 // Team and vectors per thread for a row of `vecs` 16-byte vectors of V
-// elements (SVDQ_NORM_MAX_K elements at most).
+// elements (SVDQ_NORM_MAX_K elements at most): the fewest that hold the row,
+// so that only a thread's last vector can lie past it.
 template <int V, typename F>
 cudaError_t dispatch_row(int vecs, F&& f) {
-  if (vecs <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-  if (vecs <= 64) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-  if (vecs <= 96) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 3>());
-  if (vecs <= 160) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 5>());
-  if (vecs <= 256) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
-  if (vecs <= 384) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 3>());
-  if (vecs <= 640) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 5>());
-  if (vecs <= 1024) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
-  if constexpr (V == 4)
-    if (vecs > 2048) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 8>());
+  if (vecs <= 32 * 1) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+  if (vecs <= 32 * 2) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
+  if (vecs <= 32 * 3) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 3>());
+  if (vecs <= 32 * 4) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
+  if (vecs <= 32 * 5) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 5>());
+  if (vecs <= 128 * 2) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
+  if (vecs <= 128 * 3) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 3>());
+  if (vecs <= 128 * 4) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 4>());
+  if (vecs <= 128 * 5) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 5>());
+  if (vecs <= 512 * 2) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+  if (vecs <= 512 * 3) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 3>());
+  if constexpr (V == 4) {
+    if (vecs <= 512 * 4) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+    if (vecs <= 512 * 5) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 5>());
+    if (vecs <= 512 * 6) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 6>());
+    if (vecs <= 512 * 7) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 7>());
+    return f(std::integral_constant<int, 512>(), std::integral_constant<int, 8>());
+  }
   return f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
 }
 
@@ -364,15 +570,18 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
 
 template <typename T, typename PT, int G, int NV>
 cudaError_t bwd_launch(const NormBwdArgs& a, long long groups, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(T);
-  constexpr int TEAMS = G >= 128 ? 1 : 128 / G;
+  using C = NormCfg<T, G, NV>;
   const unsigned blocks = (unsigned)(groups * a.splits);
-  const int threads = G > 128 ? G : 128;
+  static bool done[2][kMaxDevices] = {};
+  cudaError_t e;
   if (a.dw || a.db) {
-    const size_t sh = TEAMS > 1 ? sizeof(float) * 2 * NV * G * V : 0;
-    norm_bwd_kernel<T, PT, G, NV, true><<<blocks, threads, sh, st>>>(a);
+    e = allow_smem(norm_bwd_kernel<T, PT, G, NV, true>, C::BWD_SMEM, done[0]);
+    if (e != cudaSuccess) return e;
+    norm_bwd_kernel<T, PT, G, NV, true><<<blocks, C::THREADS, C::BWD_SMEM, st>>>(a);
   } else {
-    norm_bwd_kernel<T, PT, G, NV, false><<<blocks, threads, 0, st>>>(a);
+    e = allow_smem(norm_bwd_kernel<T, PT, G, NV, false>, C::BWD_SMEM, done[1]);
+    if (e != cudaSuccess) return e;
+    norm_bwd_kernel<T, PT, G, NV, false><<<blocks, C::THREADS, C::BWD_SMEM, st>>>(a);
   }
   return cudaGetLastError();
 }
@@ -435,7 +644,7 @@ svdq_status svdq_layer_norm(int dtype, int param_dtype, int M, int K, const void
   svdq::NormArgs a{};
   a.x = X; a.w = weight; a.b = bias; a.y = Y; a.mean = mean; a.rstd = rstd;
   a.ldx = ldx; a.ldw = ldw; a.ldb = ldb; a.ldy = ldy;
-  a.M = M; a.K = K; a.rows_per_group = rows_per_group;
+  a.M = M; a.K = K; a.rows_per_group = rows_per_group ? rows_per_group : M;
   a.w0 = weight_offset; a.eps = eps;
   const cudaError_t e = svdq::dispatch_types(dtype, param_dtype, [&](auto t, auto pt) {
     return svdq::fwd<decltype(t), decltype(pt)>(a, stream);
