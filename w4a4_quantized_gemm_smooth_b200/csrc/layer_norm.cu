@@ -56,7 +56,7 @@ __device__ __forceinline__ RowSpan block_span(int M, int rows_per_group, int spl
 }
 
 // How a row of up to G NV V elements (V = 16 / sizeof(T)) is held: threads of
-// a block, teams of a block, rows in flight per team, and whether the scale
+// a block, teams of a block, rows at a time and in flight per team, and whether the scale
 // and shift are kept in shared memory (not for the longest rows, which need
 // the room; they are read from the caches).
 template <typename T, int G, int NV>
@@ -65,10 +65,11 @@ struct NormCfg {
   static constexpr int THREADS = G > 128 ? G : 128;
   static constexpr int TEAMS = THREADS / G;
   static constexpr bool PSMEM = G < 512;
-  static constexpr int DF = G < 512 ? 3 : 2;                   // rows in flight, forward
+  static constexpr int RF = G < 512 ? 2 : 1;                   // rows at a time, forward
+  static constexpr int DF = 2;                                 // and steps in flight
   static constexpr int DB = NV < 8 ? 2 : 1;                    // backward (x and dy)
   static constexpr size_t PARAM = PSMEM ? (size_t)NV * G * V * 4 : 0;   // one fp32 row
-  static constexpr size_t RING_FWD = (size_t)DF * NV * THREADS * 16;
+  static constexpr size_t RING_FWD = (size_t)DF * RF * NV * THREADS * 16;
   static constexpr size_t RING_BWD = (size_t)DB * 2 * NV * THREADS * 16;
   static constexpr size_t FWD_SMEM = RING_FWD + 2 * PARAM;
   static constexpr size_t BWD_SMEM = RING_BWD + PARAM;
@@ -98,20 +99,34 @@ struct RowShare {
   }
 };
 
-// A parameter row as fp32 in shared memory: float4 k of a thread's vector i
-// at (i V / 4 + k) G + lane, so that a warp reads consecutive float4s.
-template <typename PT, int V, int G, int NV>
-__device__ __forceinline__ void stage_param(float4* dst, const PT* row, int K, int lane, float add) {
+// A parameter row as fp32 in shared memory: float4 k of vector i of lane l
+// at (i V / 4 + k) G + l, so that a warp reads consecutive float4s.  Every
+// thread of the block takes vectors in turn.
+template <typename PT, int V, int G, int NV, int THREADS>
+struct ParamStage {
+  static constexpr int N = (NV * G + THREADS - 1) / THREADS;
+  RowVec<PT, V> q[N];
+  __device__ __forceinline__ void load(const PT* row, int K) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const RowVec<PT, V> q = load_vec<PT, V>(row, (lane + i * G) * V, K);
-#pragma unroll
-    for (int k = 0; k < V / 4; ++k) {
-      const float2 a = q.get(2 * k), b = q.get(2 * k + 1);
-      dst[(i * (V / 4) + k) * G + lane] = make_float4(a.x + add, a.y + add, b.x + add, b.y + add);
+    for (int n = 0; n < N; ++n) {
+      const int u = threadIdx.x + n * THREADS;
+      if (u < NV * G) q[n] = load_vec<PT, V>(row, u * V, K);
     }
   }
-}
+  __device__ __forceinline__ void store(float4* dst, float add) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int u = threadIdx.x + n * THREADS;
+      if (u < NV * G) {
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) {
+          const float2 a = q[n].get(2 * k), b = q[n].get(2 * k + 1);
+          dst[(u / G * (V / 4) + k) * G + u % G] = make_float4(a.x + add, a.y + add, b.x + add, b.y + add);
+        }
+      }
+    }
+  }
+};
 // Pairs of a thread's vector i: from shared memory, or from the row itself.
 template <typename PT, int V, int G, bool SMEM>
 __device__ __forceinline__ void read_param(float2 (&out)[V / 2], const float4* staged, const PT* row,
@@ -130,22 +145,29 @@ __device__ __forceinline__ void read_param(float2 (&out)[V / 2], const float4* s
   }
 }
 
-// Sum over a team of G threads (G = 32: the warp; else the whole block).
-// `red` has room for G / 32 values per phase; successive calls alternate
-// between two phases, so that one barrier per call is enough.
-template <int G>
-__device__ __forceinline__ float team_sum(float v, float* red, int phase) {
-  v = warp_sum(v);
+// Sums over a team of G threads (G = 32: the warp; else the whole block) of
+// R values.  `red` has room for R G / 32 values; successive calls alternate
+// between two of them, so that one barrier per call is enough.
+template <int G, int R>
+__device__ __forceinline__ void team_sum(float (&v)[R], float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
   if constexpr (G > 32) {
     constexpr int W = G / 32;
-    float* r = red + phase * W;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0f;
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v += r[i];
+      for (int k = 0; k < R; ++k) red[k * W + (threadIdx.x >> 5)] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      v[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[k] += red[k * W + i];
+    }
   }
-  return v;
 }
 
 template <int H>
@@ -157,106 +179,125 @@ __device__ __forceinline__ float sum_pairs(const float2 (&a)[H]) {
 }
 
 template <typename T, typename PT, int G, int NV>
-__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 5 : 1)
+__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 4 : 1)
 norm_kernel(const NormArgs p) {
   using C = NormCfg<T, G, NV>;
-  constexpr int V = C::V, H = C::H, D = C::DF, TH = C::THREADS;
+  constexpr int V = C::V, H = C::H, D = C::DF, TH = C::THREADS, R = C::RF;
   extern __shared__ uint4 smem[];
-  __shared__ float red[2 * (G > 32 ? G / 32 : 1)];
+  __shared__ float red[2 * R * (G > 32 ? G / 32 : 1)];
   const int lane = threadIdx.x % G, team = threadIdx.x / G;
   const RowSpan span = block_span(p.M, p.rows_per_group, p.splits);
   const T* x = static_cast<const T*>(p.x);
-  const uint4* ring = smem + threadIdx.x;              // vector (slot, i) at (slot NV + i) TH
+  const uint4* ring = smem + threadIdx.x;              // vector (slot, row, i) at ((slot R + row) NV + i) TH
   const uint32_t ring_u = smem_u32(ring);
   float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_FWD);
   float4* pb = pw + C::PARAM / 16;
   const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
   const PT* b = p.b ? static_cast<const PT*>(p.b) + span.g * p.ldb : nullptr;
   const RowShare<T, G, NV> share(lane, p.K);
+  // the parameters' loads leave first, the rows' copies next to them
+  ParamStage<PT, V, G, C::PSMEM ? NV : 1, TH> sw, sb;
+  if constexpr (C::PSMEM) {
+    if (w) sw.load(w, p.K);
+    if (b) sb.load(b, p.K);
+  }
   auto fetch = [&](long long row, int slot) {
-    if (row < span.r1) share.fetch(x + row * p.ldx, lane, ring_u + slot * NV * TH * 16, TH * 16);
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (row + k < span.r1)
+        share.fetch(x + (row + k) * p.ldx, lane, ring_u + (slot * R + k) * NV * TH * 16, TH * 16);
     cp_async_commit();
   };
 #pragma unroll
-  for (int d = 0; d < D; ++d) fetch(span.r0 + team + d * C::TEAMS, d);
+  for (int d = 0; d < D; ++d) fetch(span.r0 + (team + d * C::TEAMS) * R, d);
   if constexpr (C::PSMEM) {
-    if (team == 0) {
-      if (w) stage_param<PT, V, G, NV>(pw, w, p.K, lane, p.w0);
-      if (b) stage_param<PT, V, G, NV>(pb, b, p.K, lane, 0.0f);
-    }
-    if (C::TEAMS > 1) __syncthreads();
+    if (w) sw.store(pw, p.w0);
+    if (b) sb.store(pb, 0.0f);
+    __syncthreads();
   }
   const float inv_k = 1.0f / (float)p.K;
   const bool ragged = p.K % V != 0;
   int slot = 0;
-  for (long long row = span.r0 + team; row < span.r1; row += C::TEAMS) {
+  // R rows at a time: their sums overlap, and the parameters are read once
+  for (long long row = span.r0 + team * R; row < span.r1; row += C::TEAMS * R) {
     cp_async_wait<D - 1>();
-    float2 v[NV][H];
-    float2 acc[H];                        // independent sums, short chains
+    float2 v[R][NV][H];
+    float sum[R], rstd[R], mu[R];
 #pragma unroll
-    for (int j = 0; j < H; ++j) acc[j] = make_float2(0.0f, 0.0f);
+    for (int k = 0; k < R; ++k) {
+      float2 acc[H];                      // independent sums, short chains
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const RowVec<T, V> q = read_vec<T, V>(ring + (slot * NV + i) * TH, TH);
+      for (int j = 0; j < H; ++j) acc[j] = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < H; ++j) {
-        v[i][j] = q.get(j);
-        acc[j] = __fadd2_rn(acc[j], v[i][j]);
-      }
-    }
-    const float mu = team_sum<G>(sum_pairs(acc), red, 0) * inv_k;
-    // every value of the slot is in registers: the row D further on may land there
-    fetch(row + (long long)D * C::TEAMS, slot);
-    slot = slot + 1 == D ? 0 : slot + 1;
-#pragma unroll
-    for (int j = 0; j < H; ++j) acc[j] = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      const float2 m = splat2(i + 1 < NV || c < p.K ? -mu : 0.0f);   // what lies past the row stays 0
-#pragma unroll
-      for (int j = 0; j < H; ++j) v[i][j] = __fadd2_rn(v[i][j], m);
-      if (i + 1 == NV && ragged && c + V > p.K) {
+      for (int i = 0; i < NV; ++i) {
+        const RowVec<T, V> q = read_vec<T, V>(ring + ((slot * R + k) * NV + i) * TH, TH);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-          if (c + 2 * j >= p.K) v[i][j].x = 0.0f;
-          if (c + 2 * j + 1 >= p.K) v[i][j].y = 0.0f;
+          v[k][i][j] = q.get(j);
+          acc[j] = __fadd2_rn(acc[j], v[k][i][j]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < H; ++j) acc[j] = __ffma2_rn(v[i][j], v[i][j], acc[j]);
+      sum[k] = sum_pairs(acc);
     }
-    const float rstd = 1.0f / sqrtf(team_sum<G>(sum_pairs(acc), red, 1) * inv_k + p.eps);
+    team_sum<G, R>(sum, red);
+    // every value of the slot is in registers: the rows D steps on may land there
+    fetch(row + (long long)D * C::TEAMS * R, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      mu[k] = sum[k] * inv_k;
+      float2 acc[H];
+#pragma unroll
+      for (int j = 0; j < H; ++j) acc[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * G) * V;
+        const float2 m = splat2(i + 1 < NV || c < p.K ? -mu[k] : 0.0f);   // what lies past the row stays 0
+#pragma unroll
+        for (int j = 0; j < H; ++j) v[k][i][j] = __fadd2_rn(v[k][i][j], m);
+        if (i + 1 == NV && ragged && c + V > p.K) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            if (c + 2 * j >= p.K) v[k][i][j].x = 0.0f;
+            if (c + 2 * j + 1 >= p.K) v[k][i][j].y = 0.0f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) acc[j] = __ffma2_rn(v[k][i][j], v[k][i][j], acc[j]);
+      }
+      sum[k] = sum_pairs(acc);
+    }
+    team_sum<G, R>(sum, red + R * (G > 32 ? G / 32 : 1));
+#pragma unroll
+    for (int k = 0; k < R; ++k) rstd[k] = 1.0f / sqrtf(sum[k] * inv_k + p.eps);
     if (lane == 0) {
-      if (p.mean) p.mean[row] = mu;
-      if (p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (row + k < span.r1) {
+          if (p.mean) p.mean[row + k] = mu[k];
+          if (p.rstd) p.rstd[row + k] = rstd[k];
+        }
     }
     T* y = static_cast<T*>(p.y) + row * p.ldy;
-    const float2 r2 = splat2(rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * G) * V;
       if (i + 1 < NV || c < p.K) {
-        RowVec<T, V> o;
-        float2 t[H], f[H];
+        float2 fw[H], fb[H];
+        if (w) read_param<PT, V, G, C::PSMEM>(fw, pw, w, p.K, lane, i, p.w0);
+        if (b) read_param<PT, V, G, C::PSMEM>(fb, pb, b, p.K, lane, i, 0.0f);
 #pragma unroll
-        for (int j = 0; j < H; ++j) t[j] = r2;
-        if (w) {
-          read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
+        for (int k = 0; k < R; ++k) {
+          const float2 r2 = splat2(rstd[k]);
+          RowVec<T, V> o;
 #pragma unroll
-          for (int j = 0; j < H; ++j) t[j] = __fmul2_rn(r2, f[j]);
+          for (int j = 0; j < H; ++j) {
+            const float2 t = w ? __fmul2_rn(r2, fw[j]) : r2;
+            o.set(j, b ? __ffma2_rn(v[k][i][j], t, fb[j]) : __fmul2_rn(v[k][i][j], t));
+          }
+          if (k == 0 || row + k < span.r1)
+            store_vec<T, V>(y + k * p.ldy, c, i + 1 < NV ? INT_MAX : p.K, o);
         }
-        if (b) {
-          read_param<PT, V, G, C::PSMEM>(f, pb, b, p.K, lane, i, 0.0f);
-#pragma unroll
-          for (int j = 0; j < H; ++j) t[j] = __ffma2_rn(v[i][j], t[j], f[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < H; ++j) t[j] = __fmul2_rn(v[i][j], t[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < H; ++j) o.set(j, t[j]);
-        store_vec<T, V>(y, c, i + 1 < NV ? INT_MAX : p.K, o);
       }
     }
   }
@@ -295,6 +336,9 @@ norm_bwd_kernel(const NormBwdArgs p) {
   float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_BWD);
   const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
   const RowShare<T, G, NV> share(lane, p.K);
+  ParamStage<PT, V, G, C::PSMEM ? NV : 1, TH> sw;
+  if constexpr (C::PSMEM)
+    if (w) sw.load(w, p.K);
   float nmu[D], nrs[D];                      // the statistics of the rows in flight
   auto fetch = [&](long long row, int slot) {
     if (row < span.r1) {
@@ -319,8 +363,8 @@ norm_bwd_kernel(const NormBwdArgs p) {
       for (int j = 0; j < H; ++j) aw[i][j] = ab[i][j] = make_float2(0.0f, 0.0f);
   }
   if constexpr (C::PSMEM) {
-    if (w && team == 0) stage_param<PT, V, G, NV>(pw, w, p.K, lane, p.w0);
-    if (TEAMS > 1) __syncthreads();
+    if (w) sw.store(pw, p.w0);
+    __syncthreads();
   }
   int slot = 0, phase = 0;
   for (long long row = span.r0 + team; row < span.r1; row += TEAMS) {
@@ -529,7 +573,7 @@ cudaError_t fwd_launch(NormArgs a, cudaStream_t st) {
   const cudaError_t e = allow_smem(norm_kernel<T, PT, G, NV>, C::FWD_SMEM, done);
   if (e != cudaSuccess) return e;
   const long long groups = ((long long)a.M + a.rows_per_group - 1) / a.rows_per_group;
-  a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : 5, C::TEAMS);
+  a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : 4, C::TEAMS);
   norm_kernel<T, PT, G, NV><<<(unsigned)(groups * a.splits), C::THREADS, C::FWD_SMEM, st>>>(a);
   return cudaGetLastError();
 }
