@@ -7,6 +7,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace svdq {
 
 // Sticky operator error word of the current device (defined in linear16.cu).
@@ -14,18 +16,27 @@ int* op_err_address();
 
 constexpr int G_BK = 64;            // reduction elements per stage (128 bytes)
 
-struct G16Args {
+// What a product does with its sums: out = epi(sums + bias) + res, and
+// pre = sums + bias.
+struct G16Out {
   const uint16_t* bias;    // [N] or null
   const uint16_t* res;     // [M][ldr] or null
   uint16_t* out;           // [M][ldo]
   uint16_t* pre;           // [M][ldp] or null
   long long ldr, ldo, ldp;
   int M, N;
-  int kblocks;
-  int tiles_m, tiles_n, num_tiles;
   int epilogue;
   int bf16;
-  int* err;
+};
+
+// One product as its kernel gets it.  A launch carries one, or the two
+// gradients of a layer: their tiles fill the GPU together.
+struct alignas(64) G16Problem {
+  CUtensorMap a, b, y, r;
+  G16Out o;
+  int kblocks;
+  int tiles_m, tiles_n, tiles;
+  int a_bytes;             // bytes of A that arrive per stage
 };
 
 // Shared-memory descriptor of a 128-byte-swizzled operand tile.
@@ -34,18 +45,17 @@ struct G16Args {
 //   MN-major: 64-wide boxes of 64 reduction rows of 128 bytes, atoms of 8
 //     reduction rows (stride 1 KB), the next 64 rows of the operand one box
 //     (8 KB) on; 16 reduction elements further is 2 KB further.
-template <bool MN>
-__device__ __forceinline__ uint64_t g_sdesc(uint32_t saddr) {
+__device__ __forceinline__ uint64_t g_sdesc(uint32_t saddr, bool mn) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(MN ? 8192 >> 4 : 1) << 16;
+  d |= (uint64_t)(mn ? 8192 >> 4 : 1) << 16;
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
 }
-template <bool MN>
-constexpr uint64_t G_KSTEP = MN ? 2048 >> 4 : 32 >> 4;    // 16 reduction elements
+// The descriptor's step for 16 reduction elements.
+__device__ __forceinline__ uint64_t g_kstep(bool mn) { return mn ? 2048 >> 4 : 32 >> 4; }
 
 // kind::f16 instruction descriptor: fp16 or bf16 operands, fp32 D, majors.
 __device__ __forceinline__ uint32_t g_idesc(int M, int N, bool bf16, bool a_mn, bool b_mn) {
@@ -64,10 +74,69 @@ __device__ __forceinline__ bool g_elect() {
   return pred != 0;
 }
 
-__device__ __forceinline__ float g_act(float v, int epilogue) {
-  if (epilogue == SVDQ_EPI_GELU) return gelu_f(v);
-  if (epilogue == SVDQ_EPI_SILU) return v / (1.0f + __expf(-v));
-  return v;
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// For pairs: a = min(|x|, 32), e = exp(-x^2 / 2) and h = erfc(|x| / sqrt 2) / 2
+// by Abramowitz and Stegun's formula 7.1.26 (a polynomial in
+// t = 1 / (1 + 0.3275911 z) times exp(-z^2), absolute error 1.5e-7 of erfc).
+// The epilogue's erff costs as much as the products of a short reduction;
+// this form is a third of it, and its error (8e-8 of |x|) is far below a
+// 16-bit step.
+struct GaussTail {
+  float2 a, e, h;
+};
+__device__ __forceinline__ GaussTail gauss_tail(float2 x) {
+  GaussTail g;
+  g.a = make_float2(fminf(fabsf(x.x), 32.0f), fminf(fabsf(x.y), 32.0f));
+  const float2 z = __fmul2_rn(g.a, make_float2(0.70710678f, 0.70710678f));
+  const float2 d = __ffma2_rn(z, make_float2(0.3275911f, 0.3275911f), make_float2(1.0f, 1.0f));
+  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 q = __fmul2_rn(__fmul2_rn(g.a, make_float2(-0.72134752f, -0.72134752f)), g.a);
+  g.e = make_float2(ex2_approx(q.x), ex2_approx(q.y));
+  auto c = [](float v) { return make_float2(0.5f * v, 0.5f * v); };
+  float2 p = __ffma2_rn(t, c(1.061405429f), c(-1.453152027f));
+  p = __ffma2_rn(p, t, c(1.421413741f));
+  p = __ffma2_rn(p, t, c(-0.284496736f));
+  p = __ffma2_rn(p, t, c(0.254829592f));
+  g.h = __fmul2_rn(__fmul2_rn(p, t), g.e);
+  return g;
+}
+
+// The activation of two sums: GELU is x (1 - h) or, for x < 0, x h, that is
+// max(x, 0) - |x| h (|x| clamped where h is 0, so that infinity stays; the
+// maximum as a sum, so that NaN stays); SiLU is x / (1 + exp(-x)).
+__device__ __forceinline__ float2 g_act2(float2 x, int epilogue) {
+  if (epilogue == SVDQ_EPI_GELU) {
+    const GaussTail g = gauss_tail(x);
+    const float2 half = make_float2(0.5f, 0.5f);
+    const float2 pos = __ffma2_rn(x, half, __fmul2_rn(make_float2(fabsf(x.x), fabsf(x.y)), half));
+    return __ffma2_rn(make_float2(-g.a.x, -g.a.y), g.h, pos);
+  }
+  if (epilogue == SVDQ_EPI_SILU)
+    return make_float2(__fdividef(x.x, 1.0f + __expf(-x.x)), __fdividef(x.y, 1.0f + __expf(-x.y)));
+  return x;
+}
+// Its derivative: GELU's is Phi(x) + x phi(x).
+__device__ __forceinline__ float2 g_act_grad2(float2 x, int epilogue) {
+  if (epilogue == SVDQ_EPI_GELU) {
+    const GaussTail g = gauss_tail(x);
+    const float2 up = make_float2(x.x < 0.0f ? g.h.x : 1.0f - g.h.x, x.y < 0.0f ? g.h.y : 1.0f - g.h.y);
+    const float2 s = make_float2(copysignf(g.a.x, x.x), copysignf(g.a.y, x.y));
+    const float2 r = __ffma2_rn(__fmul2_rn(s, make_float2(0.39894228f, 0.39894228f)), g.e, up);
+    // the clamp loses NaN
+    return make_float2(r.x + (x.x != x.x ? x.x : 0.0f), r.y + (x.y != x.y ? x.y : 0.0f));
+  }
+  const float2 q = make_float2(__fdividef(1.0f, 1.0f + __expf(-x.x)), __fdividef(1.0f, 1.0f + __expf(-x.y)));
+  return make_float2(q.x * (1.0f + x.x * (1.0f - q.x)), q.y * (1.0f + x.y * (1.0f - q.y)));
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t u, bool bf16) {
@@ -78,6 +147,33 @@ __device__ __forceinline__ uint32_t pack2(float2 v, bool bf16) {
   if (bf16) return bf16x2_bits(v);
   const __half2 h = __float22half2_rn(v);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Bounded wait of these kernels: polls (a sleeping wait wakes late, which a
+// short product feels at every stage), looks at the clock now and then.
+// Returns false once LIMIT_NS has passed or another thread of the CTA has
+// given up.
+__device__ __forceinline__ bool g_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                       int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 63u) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > LIMIT_NS) {
+        *abort_flag = 1;
+        atomicExch(err, SVDQ_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void prefetch_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
 
 // Eight 16-bit elements [c, c + 8) of a row of n (16-byte aligned, c a
@@ -110,18 +206,207 @@ struct Operand {
   bool mn;
 };
 
-inline bool operand_map(CUtensorMap* m, const Operand& o, int box_rows, bool bf16) {
-  const auto dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (o.mn)
-    return make_map(m, o.p, dt, o.rows, o.red, (uint64_t)o.ld * 2, 64, G_BK,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
-  return make_map(m, o.p, dt, o.red, o.rows, (uint64_t)o.ld * 2, G_BK, box_rows,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
+// ---- epilogue of one box: 32 rows (a lane each) by 32 columns from col0 ----
+// r: the sums; bias: 32 floats in shared memory; place: the box's 2 KB in
+// shared memory (64-byte rows, 64-byte swizzle), which holds the residual's
+// box when there is one and receives the output.  boxed: the box leaves by a
+// TMA store, which writes whole 16-byte pieces; a ragged last box is stored
+// from here element by element instead.
+__device__ __forceinline__ bool g_boxed(const G16Out& p, int col0) {
+  return p.N % 8 == 0 || col0 + 32 <= p.N;
+}
+template <int EPI, bool BF16>
+__device__ __forceinline__ void g_epilogue_box_as(const G16Out& p, const uint32_t (&r)[32],
+                                                  const float* bias, uint8_t* place, int lane,
+                                                  int row, int col0, bool boxed) {
+  constexpr bool bf16 = BF16;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int col = col0 + 8 * u;
+    float2 v[4];
+    const float4 b0 = lds128(smem_u32(bias + 8 * u)), b1 = lds128(smem_u32(bias + 8 * u + 4));
+    const float2 bv[4] = {{b0.x, b0.y}, {b0.z, b0.w}, {b1.x, b1.y}, {b1.z, b1.w}};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = __fadd2_rn(make_float2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1])),
+                        bv[e]);
+    uint32_t o[4];
+    if (p.pre) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = pack2(v[e], bf16);
+      if (row < p.M && col < p.N)
+        store8(p.pre + (long long)row * p.ldp, col, p.N, make_uint4(o[0], o[1], o[2], o[3]));
+    }
+    if constexpr (EPI != SVDQ_EPI_NONE) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = g_act2(v[e], EPI);
+    }
+    uint4* at = reinterpret_cast<uint4*>(place + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4));
+    if (p.res) {
+      const uint4 rr = *at;
+      const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], unpack2(rw[e], bf16));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack2(v[e], bf16);
+    const uint4 o4 = make_uint4(o[0], o[1], o[2], o[3]);
+    if (boxed)
+      *at = o4;
+    else if (row < p.M && col < p.N)
+      store8(p.out + (long long)row * p.ldo, col, p.N, o4);
+  }
 }
 
+__device__ __forceinline__ void g_epilogue_box(const G16Out& p, const uint32_t (&r)[32],
+                                               const float* bias, uint8_t* place, int lane,
+                                               int row, int col0, bool boxed) {
+  auto as = [&](auto epi) {
+    constexpr int EPI = decltype(epi)::value;
+    if (p.bf16)
+      g_epilogue_box_as<EPI, true>(p, r, bias, place, lane, row, col0, boxed);
+    else
+      g_epilogue_box_as<EPI, false>(p, r, bias, place, lane, row, col0, boxed);
+  };
+  if (p.epilogue == SVDQ_EPI_GELU)
+    as(std::integral_constant<int, SVDQ_EPI_GELU>());
+  else if (p.epilogue == SVDQ_EPI_SILU)
+    as(std::integral_constant<int, SVDQ_EPI_SILU>());
+  else
+    as(std::integral_constant<int, SVDQ_EPI_NONE>());
+}
 
-// The product kernels' launchers.  Y = epi(A B^T + bias) + R with the output
-// M = A.rows by N = B.rows and the reduction A.red = B.red.
-cudaError_t launch_gemm16_pair(const Operand& A, const Operand& B, const G16Args& a, cudaStream_t st);
+// Eight sums of one row, columns [col, col + 8) (col a multiple of 8, row < M).
+__device__ __forceinline__ void g_epilogue_row(const G16Out& p, float2 (&v)[4], int row, int col) {
+  const bool bf16 = p.bf16 != 0;
+  auto add8 = [&](uint4 q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(v[e], unpack2(w[e], bf16));
+  };
+  auto store = [&](uint16_t* base, long long ld) {
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack2(v[e], bf16);
+    store8(base + (long long)row * ld, col, p.N, make_uint4(o[0], o[1], o[2], o[3]));
+  };
+  uint4 res = make_uint4(0, 0, 0, 0);
+  if (p.res) res = load8(p.res + (long long)row * p.ldr, col, p.N);
+  if (p.bias) add8(load8(p.bias, col, p.N));
+  if (p.pre) store(p.pre, p.ldp);
+  if (p.epilogue != SVDQ_EPI_NONE) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = g_act2(v[e], p.epilogue);
+  }
+  if (p.res) add8(res);
+  store(p.out, p.ldo);
+}
+
+// Cluster helpers.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address of the same shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ float lds32_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Output tile of index t: bands of 8 row tiles, walked column by column, so
+// that the tiles at work together share A and B in L2.
+struct TilePos {
+  int m, n;
+};
+__device__ __forceinline__ TilePos tile_pos(int t, int tiles_m, int tiles_n) {
+  constexpr int BAND = 8;
+  const int per = BAND * tiles_n;
+  const int band = t / per, r = t - band * per;
+  const int rows = min(BAND, tiles_m - band * BAND);
+  return {band * BAND + r % rows, r / rows};
+}
+
+// What a launch computes.  The kernels know the operands' majors from the
+// place of a problem: Forward has one, both operands K-major; Gradients has
+// dX (A K-major, B MN-major) at 0 and dW (both MN-major) at 1, of which one
+// may be missing (A.p null).  Descriptors of the MMAs are uniform this way,
+// which their issue rate needs.
+enum class G16Kind { Forward, Gradients };
+struct G16Launch {
+  G16Kind kind;
+  Operand A[2], B[2];
+  G16Out o[2];
+  int bf16;
+  int* err;
+};
+
+// Both problems of a launch; a missing one has no tiles.
+template <typename F>
+inline bool make_problems(G16Problem (&p)[2], const G16Launch& l, F&& make) {
+  int have = -1;
+  for (int i = 0; i < 2; ++i)
+    if (l.A[i].p) {
+      if (!make(&p[i], l.A[i], l.B[i], l.o[i])) return false;
+      have = i;
+    }
+  if (have < 0) return false;
+  for (int i = 0; i < 2; ++i)
+    if (!l.A[i].p) {
+      p[i] = p[have];
+      p[i].tiles = 0;
+    }
+  return true;
+}
+
+// Fills one problem for tiles of bm x bn, of which a CTA loads box_m rows of
+// A and box_n of B.  For an A of fewer rows than the box only those arrive
+// (K-major: in groups of 8); the others are never used.
+inline bool make_problem(G16Problem* p, const Operand& A, const Operand& B, const G16Out& o, int bm,
+                         int bn, int box_m, int box_n, bool boxes) {
+  const auto dt = o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  int rows = box_m;
+  if (!A.mn && A.rows < box_m) rows = (A.rows + 7) / 8 * 8;
+  auto map = [&](CUtensorMap* m, const Operand& x, int box) {
+    if (x.mn)
+      return make_map(m, x.p, dt, x.rows, x.red, (uint64_t)x.ld * 2, 64, G_BK, CU_TENSOR_MAP_SWIZZLE_128B);
+    return make_map(m, x.p, dt, x.red, x.rows, (uint64_t)x.ld * 2, G_BK, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!map(&p->a, A, rows) || !map(&p->b, B, box_n)) return false;
+  p->y = p->r = p->a;          // unused without boxes
+  if (boxes) {
+    if (!make_map(&p->y, o.out, dt, B.rows, A.rows, (uint64_t)o.ldo * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return false;
+    if (o.res && !make_map(&p->r, o.res, dt, B.rows, A.rows, (uint64_t)o.ldr * 2, 32, 32,
+                           CU_TENSOR_MAP_SWIZZLE_64B))
+      return false;
+  }
+  const long long tm = ((long long)A.rows + bm - 1) / bm, tn = ((long long)B.rows + bn - 1) / bn;
+  if (tm * tn > 0x0FFFFFFF) return false;
+  p->o = o;
+  p->o.M = A.rows;
+  p->o.N = B.rows;
+  p->kblocks = (int)(((long long)A.red + G_BK - 1) / G_BK);
+  p->tiles_m = (int)tm;
+  p->tiles_n = (int)tn;
+  p->tiles = (int)(tm * tn);
+  p->a_bytes = A.mn ? box_m * 128 : rows * 128;
+  return true;
+}
+
+// pair: 256 x bn tiles on CTA pairs; split: 128 x bn tiles, the reduction
+// divided over a cluster of `splits` CTAs.
+cudaError_t launch_gemm16_pair(const G16Launch& l, int bn, cudaStream_t st);
+cudaError_t launch_gemm16_split(const G16Launch& l, int bn, int splits, cudaStream_t st);
 
 }  // namespace svdq

@@ -27,34 +27,20 @@ template <int BN>
 struct PLay {
   static constexpr int ST_A = 128 * 128, ST_B = BN / 2 * 128;     // one CTA's share
   static constexpr int STAGE = ST_A + ST_B;
-  static constexpr int NST = BN == 256 ? 6 : BN == 192 ? 6 : 7;
+  static constexpr int NST = BN == 256 ? 5 : BN == 192 ? 6 : 8;
   static constexpr int BOX = 32 * 64;                             // 32 rows x 32 elements
-  static constexpr int OFF_Y = NST * STAGE;                       // two boxes per epilogue warp
-  static constexpr int OFF_BIAS = OFF_Y + P_EPI * 2 * BOX;        // 32 floats per epilogue warp
+  static constexpr int CH = BN / 64;                              // boxes per epilogue warp and tile
+  static constexpr int OFF_Y = NST * STAGE;                       // a place for each box
+  static constexpr int OFF_BIAS = OFF_Y + P_EPI * CH * BOX;       // 32 floats per epilogue warp
   static constexpr int OFF_BAR = OFF_BIAS + P_EPI * 128;
-  // full[NST], empty[NST], tm_full[2], tm_empty[2], residual[8][2], drain
-  static constexpr int N_BARS = 2 * NST + 4 + 2 * P_EPI + 1;
+  // full[NST], empty[NST], tm_full[2], tm_empty[2], residual[8], drain
+  static constexpr int N_BARS = 2 * NST + 4 + P_EPI + 1;
   static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
   static_assert(STAGE % 1024 == 0 && ST_A % 1024 == 0, "swizzle atoms");
   static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The address of the same shared-memory place in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -85,24 +71,10 @@ __device__ __forceinline__ void commit_pair(uint32_t mbar) {
       " [%0], %1;" ::"r"(mbar), "h"((uint16_t)3) : "memory");
 }
 
-// Output tile of index t: bands of 8 row tiles, walked column by column, so
-// that the pairs at work together share A and B in L2.
-struct TilePos {
-  int m, n;
-};
-__device__ __forceinline__ TilePos tile_pos(int t, int tiles_m, int tiles_n) {
-  constexpr int BAND = 8;
-  const int per = BAND * tiles_n;
-  const int band = t / per, r = t - band * per;
-  const int rows = min(BAND, tiles_m - band * BAND);
-  return {band * BAND + r % rows, r / rows};
-}
-
-template <int BN, bool A_MN, bool B_MN>
+template <int BN, bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
-gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
-                   const G16Args p) {
+gemm16_pair_kernel(const __grid_constant__ G16Problem p0, const __grid_constant__ G16Problem p1,
+                   const int total, const int bf16, int* err) {
   using L = PLay<BN>;
   constexpr int NST = L::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -114,18 +86,23 @@ gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   auto st_empty = [&](int s) { return bar0 + 8u * (NST + s); };
   auto tm_full = [&](int b) { return bar0 + 8u * (2 * NST + b); };
   auto tm_empty = [&](int b) { return bar0 + 8u * (2 * NST + 2 + b); };
-  auto r_full = [&](int w, int b) { return bar0 + 8u * (2 * NST + 4 + 2 * w + b); };
-  const uint32_t drain = bar0 + 8u * (2 * NST + 4 + 2 * P_EPI);
+  auto r_full = [&](int w) { return bar0 + 8u * (2 * NST + 4 + w); };
+  const uint32_t drain = bar0 + 8u * (2 * NST + 4 + P_EPI);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+  if (tid == 32) {
+    prefetch_map(&p0.a);
+    prefetch_map(&p0.b);
+    prefetch_map(&p0.y);
+  }
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) { mbar_init(st_full(s), 1); mbar_init(st_empty(s), 1); }
     for (int b = 0; b < 2; ++b) { mbar_init(tm_full(b), 1); mbar_init(tm_empty(b), 2 * P_EPI); }
-    for (int w = 0; w < P_EPI; ++w) { mbar_init(r_full(w, 0), 1); mbar_init(r_full(w, 1), 1); }
+    for (int w = 0; w < P_EPI; ++w) mbar_init(r_full(w), 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -146,26 +123,32 @@ gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       // ---------------------------------------------------- TMA producer
       uint32_t it = 0;
       bool alive = true;
-      for (int t = pair; t < p.num_tiles && alive; t += pairs) {
-        const TilePos pos = tile_pos(t, p.tiles_m, p.tiles_n);
+      for (int t = pair; t < total && alive; t += pairs) {
+        const bool first = t < p0.tiles;
+        const G16Problem& p = first ? p0 : p1;
+        const TilePos pos = tile_pos(first ? t : t - p0.tiles, p.tiles_m, p.tiles_n);
         const int m0 = pos.m * 256 + 128 * rank, n0 = pos.n * BN + BN / 2 * rank;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+        const int kblocks = p.kblocks;
+        const bool a_mn = GRAD && !first;
+        constexpr bool b_mn = GRAD;
+        const uint32_t bytes = 2 * (p.a_bytes + L::ST_B);
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int st = it % NST;
-          if (!wait_or_abort(st_empty(st), ((it / NST) & 1) ^ 1, abort_flag, p.err)) { alive = false; break; }
+          if (!g_wait(st_empty(st), ((it / NST) & 1) ^ 1, abort_flag, err)) { alive = false; break; }
           const uint32_t full = map_rank(st_full(st), 0);
-          if (rank == 0) mbar_arrive_expect_tx(st_full(st), 2 * L::STAGE);
+          if (rank == 0) mbar_arrive_expect_tx(st_full(st), bytes);
           const uint32_t da = sbase + st * L::STAGE, db = da + L::ST_A;
-          if constexpr (A_MN) {
+          if (a_mn) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) tma_load_pair(da + j * 8192, &tm_a, m0 + 64 * j, kb * G_BK, full);
+            for (int j = 0; j < 2; ++j) tma_load_pair(da + j * 8192, &p.a, m0 + 64 * j, kb * G_BK, full);
           } else {
-            tma_load_pair(da, &tm_a, kb * G_BK, m0, full);
+            tma_load_pair(da, &p.a, kb * G_BK, m0, full);
           }
-          if constexpr (B_MN) {
+          if (b_mn) {
 #pragma unroll
-            for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + j * 8192, &tm_b, n0 + 64 * j, kb * G_BK, full);
+            for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + j * 8192, &p.b, n0 + 64 * j, kb * G_BK, full);
           } else {
-            tma_load_pair(db, &tm_b, kb * G_BK, n0, full);
+            tma_load_pair(db, &p.b, kb * G_BK, n0, full);
           }
         }
       }
@@ -178,30 +161,36 @@ gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   } else if (warp == 1) {
     if (rank == 0) {
       // ------------------------------------------------------ MMA issuer
-      const uint32_t idesc = g_idesc(256, BN, p.bf16 != 0, A_MN, B_MN);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
         int ok = 1;
-        if (lane == 0) ok = wait_or_abort(bar, parity, abort_flag, p.err) ? 1 : 0;
+        if (lane == 0) ok = g_wait(bar, parity, abort_flag, err) ? 1 : 0;
         return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
       };
       uint32_t it = 0, tb = 0;
       bool ok = true;
-      for (int t = pair; t < p.num_tiles; t += pairs, ++tb) {
+      for (int t = pair; t < total; t += pairs, ++tb) {
         const int b = tb & 1;
         if (!wait_warp(tm_empty(b), ((tb >> 1) & 1) ^ 1)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tm + b * 256;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+        // read from the parameters themselves: uniform
+        const bool first = t < p0.tiles;
+        const bool a_mn = GRAD && !first;
+        constexpr bool b_mn = GRAD;
+        const uint32_t idesc = g_idesc(256, BN, bf16 != 0, a_mn, b_mn);
+        const uint64_t ak = g_kstep(a_mn), bk = g_kstep(b_mn);
+        const int kblocks = first ? p0.kblocks : p1.kblocks;
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int st = it % NST;
           if (!wait_warp(st_full(st), (it / NST) & 1)) { ok = false; break; }
           tc_fence_after();
           if (g_elect()) {
-            const uint64_t ad = g_sdesc<A_MN>(sbase + st * L::STAGE);
-            const uint64_t bd = g_sdesc<B_MN>(sbase + st * L::STAGE + L::ST_A);
+            const uint64_t ad = g_sdesc(sbase + st * L::STAGE, a_mn);
+            const uint64_t bd = g_sdesc(sbase + st * L::STAGE + L::ST_A, b_mn);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_pair(d, ad + j * G_KSTEP<A_MN>, bd + j * G_KSTEP<B_MN>, idesc,
+              mma_pair(d, ad + j * ak, bd + j * bk, idesc,
                        (kb > 0 || j > 0) ? 1u : 0u);
             commit_pair(st_empty(st));
           }
@@ -222,17 +211,19 @@ gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   } else if (warp >= P_EPI0) {
     // ------------------------------------------------------ epilogue
     const int w = warp - P_EPI0, q = warp & 3, half = w >> 2;
-    constexpr int CH = BN / 64;                       // 32-column boxes of this warp
+    constexpr int CH = L::CH;                         // 32-column boxes of this warp
     const uint32_t lane_off = (uint32_t)(32 * q) << 16;
-    uint8_t* stage = smem + L::OFF_Y + w * 2 * L::BOX;
+    uint8_t* stage = smem + L::OFF_Y + w * CH * L::BOX;
     const uint32_t stage_u = smem_u32(stage);
     float* bias_s = reinterpret_cast<float*>(smem + L::OFF_BIAS + w * 128);
-    const bool bf16 = p.bf16 != 0, has_r = p.res != nullptr;
     const uint32_t tm_empty0[2] = {map_rank(tm_empty(0), 0), map_rank(tm_empty(1), 0)};
-    uint32_t tb = 0, cc = 0;                          // tiles and boxes so far
-    bool alive = true;
-    for (int t = pair; t < p.num_tiles && alive; t += pairs, ++tb) {
-      const TilePos pos = tile_pos(t, p.tiles_m, p.tiles_n);
+    uint32_t tb = 0, rb = 0;                          // tiles so far, and those with a residual
+    for (int t = pair; t < total; t += pairs, ++tb) {
+      const bool first = t < p0.tiles;
+      const G16Problem& pr = first ? p0 : p1;
+      const G16Out p = pr.o;
+      const bool has_r = p.res != nullptr;
+      const TilePos pos = tile_pos(first ? t : t - p0.tiles, pr.tiles_m, pr.tiles_n);
       const int m0 = pos.m * 256 + 128 * rank + 32 * q, n0 = pos.n * BN + BN / 2 * half;
       const int b = tb & 1;
       const int row = m0 + lane;
@@ -240,98 +231,56 @@ gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = n0 + 32 * c + lane;
-        bias[c] = p.bias && col < p.N ? unpack2(__ldg(p.bias + col), bf16).x : 0.0f;
+        bias[c] = p.bias && col < p.N ? unpack2(__ldg(p.bias + col), p.bf16 != 0).x : 0.0f;
       }
-      auto load_r = [&](int c, uint32_t buf) {        // lane 0: the residual's box c
-        tma_store_wait_read0();
-        mbar_arrive_expect_tx(r_full(w, buf), L::BOX);
-        tma_load_2d(stage_u + buf * L::BOX, &tm_r, n0 + 32 * c, m0, r_full(w, buf));
-      };
-      if (has_r && lane == 0) load_r(0, cc & 1);
-      if (!wait_or_abort(tm_full(b), (tb >> 1) & 1, abort_flag, p.err)) alive = false;
-      alive = __all_sync(0xFFFFFFFFu, alive);
-      if (!alive) {
-        // the residual's box in flight lands before the CTA ends
-        if (has_r) mbar_wait_bounded(r_full(w, cc & 1), (cc >> 1) & 1, LIMIT_NS);
-        break;
+      if (lane == 0) {
+        tma_store_wait_read0();                       // the previous tile's boxes have left
+        if (has_r) {
+          mbar_arrive_expect_tx(r_full(w), CH * L::BOX);
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            tma_load_2d(stage_u + c * L::BOX, &pr.r, n0 + 32 * c, m0, r_full(w));
+        }
       }
+      bool alive = g_wait(tm_full(b), (tb >> 1) & 1, abort_flag, err);
+      if (has_r) {
+        // also after an expired wait: the boxes land before the CTA ends
+        alive = mbar_wait_bounded(r_full(w), rb & 1, LIMIT_NS) && alive;
+        ++rb;
+      }
+      if (!__all_sync(0xFFFFFFFFu, alive)) break;
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < CH; ++c, ++cc) {
-        const uint32_t buf = cc & 1;
-        if (lane == 0) {
-          if (has_r) {
-            if (c + 1 < CH) load_r(c + 1, buf ^ 1);
-          } else {
-            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          }
-        }
-        uint32_t r[32];
-        tmem_ld32(tmem + b * 256 + BN / 2 * half + 32 * c + lane_off, r);
-        bias_s[lane] = bias[c];
+      for (int c = 0; c < CH; c += 2) {
+        constexpr int TWO = 2;
+        uint32_t r[TWO][32];
+        const int n = CH - c < TWO ? CH - c : TWO;    // known at compile time
+#pragma unroll
+        for (int k = 0; k < n; ++k) tmem_ld32(tmem + b * 256 + BN / 2 * half + 32 * (c + k) + lane_off, r[k]);
         tmem_wait_ld();
-        if (c + 1 == CH) {                            // the accumulator may be overwritten
+        if (c + TWO >= CH) {                          // the accumulator may be overwritten
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(tm_empty0[b]);
         }
-        __syncwarp();
-        if (has_r && !wait_or_abort(r_full(w, buf), (cc >> 1) & 1, abort_flag, p.err)) alive = false;
-        uint8_t* yrow = stage + buf * L::BOX + lane * 64;
-        // a TMA store writes whole 16-byte pieces: a ragged last box leaves
-        // by element stores instead
-        const bool boxed = p.N % 8 == 0 || n0 + 32 * c + 32 <= p.N;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float v[8];
-          const float4 b0 = lds128(smem_u32(bias_s + 8 * u)), b1 = lds128(smem_u32(bias_s + 8 * u + 4));
-          const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * u + e]) + bv[e];
-          if (p.pre) {
-            const int col = n0 + 32 * c + 8 * u;
-            if (row < p.M && col < p.N) {
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = pack2(make_float2(v[2 * e], v[2 * e + 1]), bf16);
-              store8(p.pre + (long long)row * p.ldp, col, p.N, make_uint4(o[0], o[1], o[2], o[3]));
-            }
+        for (int k = 0; k < n; ++k) {
+          const int col0 = n0 + 32 * (c + k);
+          __syncwarp();
+          bias_s[lane] = bias[c + k];
+          __syncwarp();
+          const bool boxed = g_boxed(p, col0);
+          g_epilogue_box(p, r[k], bias_s, stage + (c + k) * L::BOX, lane, row, col0, boxed);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && boxed) {
+            tma_store_2d(&pr.y, col0, m0, stage_u + (c + k) * L::BOX);
+            tma_store_commit();
           }
-          if (p.epilogue != SVDQ_EPI_NONE) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = g_act(v[e], p.epilogue);
-          }
-          uint4* place = reinterpret_cast<uint4*>(yrow + ((u ^ ((lane >> 1) & 3)) << 4));
-          if (has_r) {
-            const uint4 rr = *place;
-            const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2(rw[e], bf16);
-              v[2 * e] += f.x;
-              v[2 * e + 1] += f.y;
-            }
-          }
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = pack2(make_float2(v[2 * e], v[2 * e + 1]), bf16);
-          const uint4 o4 = make_uint4(o[0], o[1], o[2], o[3]);
-          const int col = n0 + 32 * c + 8 * u;
-          if (boxed)
-            *place = o4;
-          else if (row < p.M && col < p.N)
-            store8(p.out + (long long)row * p.ldo, col, p.N, o4);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (boxed) tma_store_2d(&tm_y, n0 + 32 * c, m0, stage_u + buf * L::BOX);
-          tma_store_commit();         // an empty group keeps the count of groups
         }
       }
-      alive = __all_sync(0xFFFFFFFFu, alive);
     }
-    if (lane == 0) tma_store_wait0();
+    if (lane == 0) tma_store_wait_read0();      // the boxes have left; the grid's end orders the writes
     __syncwarp();
   }
 
@@ -344,52 +293,37 @@ gemm16_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   }
 }
 
-template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch_bn(const Operand& A, const Operand& B, G16Args a, cudaStream_t st) {
+template <int BN, bool GRAD>
+cudaError_t launch_bn(const G16Launch& l, cudaStream_t st) {
   using L = PLay<BN>;
   static bool attr[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm16_pair_kernel<BN, A_MN, B_MN>,
+    const cudaError_t e = cudaFuncSetAttribute(gemm16_pair_kernel<BN, GRAD>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
     if (e != cudaSuccess) return e;
     attr[dev] = true;
   }
-  const bool bf16 = a.bf16 != 0;
-  const auto dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap ta, tb, ty, tr;
-  if (!operand_map(&ta, A, 128, bf16) || !operand_map(&tb, B, BN / 2, bf16) ||
-      !make_map(&ty, a.out, dt, B.rows, A.rows, (uint64_t)a.ldo * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+  G16Problem p[2];
+  if (!make_problems(p, l, [](G16Problem* q, const Operand& A, const Operand& B, const G16Out& o) {
+        return make_problem(q, A, B, o, 256, BN, 128, BN / 2, true);
+      }))
     return cudaErrorInvalidValue;
-  tr = ty;
-  if (a.res && !make_map(&tr, a.res, dt, B.rows, A.rows, (uint64_t)a.ldr * 2, 32, 32,
-                         CU_TENSOR_MAP_SWIZZLE_64B))
-    return cudaErrorInvalidValue;
-  const long long tm = ((long long)A.rows + 255) / 256, tn = ((long long)B.rows + BN - 1) / BN;
-  if (tm * tn > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-  a.M = A.rows;
-  a.N = B.rows;
-  a.kblocks = (int)(((long long)A.red + G_BK - 1) / G_BK);
-  a.tiles_m = (int)tm;
-  a.tiles_n = (int)tn;
-  a.num_tiles = (int)(tm * tn);
-  const int pairs = a.num_tiles < num_sms() / 2 ? a.num_tiles : num_sms() / 2;
-  gemm16_pair_kernel<BN, A_MN, B_MN><<<2 * pairs, P_THREADS, L::ALLOC, st>>>(ta, tb, ty, tr, a);
+  const int total = p[0].tiles + p[1].tiles;
+  const int pairs = total < num_sms() / 2 ? total : num_sms() / 2;
+  gemm16_pair_kernel<BN, GRAD><<<2 * pairs, P_THREADS, L::ALLOC, st>>>(p[0], p[1], total, l.bf16, l.err);
   return cudaGetLastError();
-}
-
-template <bool A_MN, bool B_MN>
-cudaError_t launch_major(const Operand& A, const Operand& B, const G16Args& a, cudaStream_t st) {
-  return launch_bn<256, A_MN, B_MN>(A, B, a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm16_pair(const Operand& A, const Operand& B, const G16Args& a, cudaStream_t st) {
-  if (A.mn) return launch_major<true, true>(A, B, a, st);
-  if (B.mn) return launch_major<false, true>(A, B, a, st);
-  return launch_major<false, false>(A, B, a, st);
+cudaError_t launch_gemm16_pair(const G16Launch& l, int bn, cudaStream_t st) {
+  if (l.kind == G16Kind::Gradients)      // half of 192 MN-major columns is no whole number of boxes
+    return bn == 128 ? launch_bn<128, true>(l, st) : launch_bn<256, true>(l, st);
+  if (bn == 128) return launch_bn<128, false>(l, st);
+  if (bn == 192) return launch_bn<192, false>(l, st);
+  return launch_bn<256, false>(l, st);
 }
 
 }  // namespace svdq

@@ -1,5 +1,6 @@
 // 16-bit linear layer (bf16 or fp16 operands, fp32 accumulation on the
-// tensor cores) and its gradients: three products of one kernel,
+// tensor cores) and its gradients: the entry points, the activation's
+// gradient, and the choice among the product kernels.  Three products:
 //   Y  = epi(X W^T + b) + R      A = X   (K-major), B = W (K-major)
 //   dX = dP W                    A = dP  (K-major), B = W^T (MN-major)
 //   dW = dP^T X                  A = dP^T, B = X^T  (both MN-major)
@@ -7,11 +8,7 @@
 // axis is contiguous in memory is K-major; one whose other axis is, is
 // MN-major: TMA brings both as 128-byte-swizzled boxes, and the MMA's
 // descriptors say which way they lie, so no transposed copy is ever made.
-//
-// Warp-specialised persistent CTAs, one per SM: warp 0 issues TMA, warp 1
-// the tcgen05.mma kind::f16, warps 4-7 the epilogue; two TMEM accumulators
-// let a tile accumulate while the previous one is stored.  Every wait is
-// bounded (the device's operator error word is raised on expiry).
+// Both gradients go out in one launch.
 #include "elem.cuh"
 #include "gemm16.cuh"
 
@@ -33,215 +30,8 @@ int* op_err_address() {
 
 namespace {
 
-constexpr int G_THREADS = 256;
-constexpr int G_EPI0 = 4;           // epilogue warps 4-7
-
-template <int BN>
-struct GLay {
-  static constexpr int BM = 128;
-  static constexpr int ST_A = BM * 128, ST_B = BN * 128;
-  static constexpr int STAGE = ST_A + ST_B;
-  static constexpr int NST = 4;
-  static constexpr int OFF_BAR = NST * STAGE;
-  static constexpr int N_BARS = 2 * NST + 5;      // the last one: drain after an expired wait
-  static constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
-  static constexpr int ALLOC = OFF_MISC + 16 + 1024;
-  static_assert(ALLOC <= 227 * 1024, "shared memory");
-};
-
-template <int BN, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(G_THREADS, 1)
-gemm16_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-              const G16Args p) {
-  using L = GLay<BN>;
-  constexpr int BM = L::BM, NST = L::NST;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar0 = sbase + L::OFF_BAR;
-  auto st_full = [&](int s) { return bar0 + 8u * s; };
-  auto st_empty = [&](int s) { return bar0 + 8u * (NST + s); };
-  auto tm_full = [&](int b) { return bar0 + 8u * (2 * NST + b); };
-  auto tm_empty = [&](int b) { return bar0 + 8u * (2 * NST + 2 + b); };
-  const uint32_t drain = bar0 + 8u * (2 * NST + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-  int* err = p.err;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  if (tid == 0) {
-    for (int s = 0; s < NST; ++s) { mbar_init(st_full(s), 1); mbar_init(st_empty(s), 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(tm_full(b), 1); mbar_init(tm_empty(b), 4); }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 2 * BN);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool alive = true;
-      for (int t = blockIdx.x; t < p.num_tiles && alive; t += gridDim.x) {
-        const int m0 = (t % p.tiles_m) * BM, n0 = (t / p.tiles_m) * BN;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const int st = it % NST;
-          if (!wait_or_abort(st_empty(st), ((it / NST) & 1) ^ 1, abort_flag, err)) { alive = false; break; }
-          mbar_arrive_expect_tx(st_full(st), L::STAGE);
-          const uint32_t da = sbase + st * L::STAGE, db = da + L::ST_A;
-          if constexpr (A_MN) {
-#pragma unroll
-            for (int j = 0; j < BM / 64; ++j)
-              tma_load_2d(da + j * 8192, &tm_a, m0 + 64 * j, kb * G_BK, st_full(st));
-          } else {
-            tma_load_2d(da, &tm_a, kb * G_BK, m0, st_full(st));
-          }
-          if constexpr (B_MN) {
-#pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(db + j * 8192, &tm_b, n0 + 64 * j, kb * G_BK, st_full(st));
-          } else {
-            tma_load_2d(db, &tm_b, kb * G_BK, n0, st_full(st));
-          }
-        }
-      }
-      // no copy is in flight when the CTA ends
-      for (uint32_t k = (it > NST ? it - NST : 0); k < it; ++k)
-        mbar_wait_bounded(st_full(k % NST), (k / NST) & 1, LIMIT_NS);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    const uint32_t idesc = g_idesc(BM, BN, p.bf16 != 0, A_MN, B_MN);
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
-      int ok = 1;
-      if (lane == 0) ok = wait_or_abort(bar, parity, abort_flag, err) ? 1 : 0;
-      return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-    };
-    uint32_t it = 0, tb = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < p.num_tiles; t += gridDim.x, ++tb) {
-      const int b = tb & 1;
-      if (!wait_warp(tm_empty(b), ((tb >> 1) & 1) ^ 1)) { ok = false; break; }
-      tc_fence_after();
-      const uint32_t d = tm + b * BN;
-      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-        const int st = it % NST;
-        if (!wait_warp(st_full(st), (it / NST) & 1)) { ok = false; break; }
-        tc_fence_after();
-        if (g_elect()) {
-          const uint64_t ad = g_sdesc<A_MN>(sbase + st * L::STAGE);
-          const uint64_t bd = g_sdesc<B_MN>(sbase + st * L::STAGE + L::ST_A);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_bf16(d, ad + j * G_KSTEP<A_MN>, bd + j * G_KSTEP<B_MN>, idesc,
-                     (kb > 0 || j > 0) ? 1u : 0u);
-          mma_commit(st_empty(st));
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (g_elect()) mma_commit(tm_full(b));
-      __syncwarp();
-    }
-    // after an expired wait, TMEM is freed only once the issued MMAs are done
-    if (!ok && g_elect()) {
-      mma_commit(drain);
-      mbar_wait_bounded(drain, 0, LIMIT_NS);
-    }
-    __syncwarp();
-  } else if (warp >= G_EPI0) {
-    const int q = warp & 3;
-    const uint32_t lane_off = (uint32_t)(32 * q) << 16;
-    const bool bf16 = p.bf16 != 0;
-    uint32_t tb = 0;
-    for (int t = blockIdx.x; t < p.num_tiles; t += gridDim.x, ++tb) {
-      const int m0 = (t % p.tiles_m) * BM, n0 = (t / p.tiles_m) * BN;
-      const int row = m0 + 32 * q + lane;
-      const int b = tb & 1;
-      if (!wait_or_abort(tm_full(b), (tb >> 1) & 1, abort_flag, err)) break;
-      tc_fence_after();
-      __syncwarp();
-#pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tmem + b * BN + 32 * c + lane_off, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int col = n0 + 32 * c + 8 * u;
-          if (row < p.M && col < p.N) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * u + e]);
-            if (p.bias) {
-              const uint4 bb = load8(p.bias, col, p.N);
-              const uint32_t w[4] = {bb.x, bb.y, bb.z, bb.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack2(w[e], bf16);
-                v[2 * e] += f.x;
-                v[2 * e + 1] += f.y;
-              }
-            }
-            if (p.pre) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = pack2(make_float2(v[2 * e], v[2 * e + 1]), bf16);
-              store8(p.pre + (long long)row * p.ldp, col, p.N, make_uint4(w[0], w[1], w[2], w[3]));
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = g_act(v[e], p.epilogue);
-            if (p.res) {
-              const uint4 bb = load8(p.res + (long long)row * p.ldr, col, p.N);
-              const uint32_t w[4] = {bb.x, bb.y, bb.z, bb.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack2(w[e], bf16);
-                v[2 * e] += f.x;
-                v[2 * e + 1] += f.y;
-              }
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack2(make_float2(v[2 * e], v[2 * e + 1]), bf16);
-            store8(p.out + (long long)row * p.ldo, col, p.N, make_uint4(w[0], w[1], w[2], w[3]));
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tm_empty(b));
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
-  }
-}
-
 // ------------------------------------------------ activation's gradient
 // dP = dY epi'(P) rounded to 16 bits, and the column sums of its fp32 values.
-__device__ __forceinline__ float g_act_grad(float x, int epilogue) {
-  if (epilogue == SVDQ_EPI_GELU) {
-    const float phi = 0.3989422804014327f * __expf(-0.5f * x * x);
-    return 0.5f * (1.0f + erff(x * 0.70710678118654752f)) + x * phi;
-  }
-  const float s = 1.0f / (1.0f + __expf(-x));
-  return s * (1.0f + x * (1.0f - s));
-}
-
 struct DpArgs {
   const uint16_t* dy;
   const uint16_t* p;       // pre-activation, null without an activation
@@ -271,10 +61,7 @@ dp_kernel(const DpArgs a) {
         const uint32_t pw[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float2 d = unpack2(dw[e], bf16);
-          const float2 x = unpack2(pw[e], bf16);
-          d.x *= g_act_grad(x.x, a.epilogue);
-          d.y *= g_act_grad(x.y, a.epilogue);
+          const float2 d = __fmul2_rn(unpack2(dw[e], bf16), g_act_grad2(unpack2(pw[e], bf16), a.epilogue));
           acc[2 * e] += d.x;
           acc[2 * e + 1] += d.y;
           dw[e] = pack2(d, bf16);
@@ -336,41 +123,75 @@ int dp_row_blocks(int M, int N) {
 }
 
 // --------------------------------------------------------------- launches
-template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch_gemm_bn(const Operand& A, const Operand& B, G16Args a, cudaStream_t st) {
-  using L = GLay<BN>;
-  static bool attr[kMaxDevices] = {};
-  const int dev = current_device();
-  if (dev < 0) return cudaErrorInvalidDevice;
-  if (!attr[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm16_kernel<BN, A_MN, B_MN>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
-    if (e != cudaSuccess) return e;
-    attr[dev] = true;
-  }
-  CUtensorMap ta, tb;
-  if (!operand_map(&ta, A, L::BM, a.bf16 != 0) || !operand_map(&tb, B, BN, a.bf16 != 0))
-    return cudaErrorInvalidValue;
-  const long long tm = ((long long)A.rows + L::BM - 1) / L::BM, tn = ((long long)B.rows + BN - 1) / BN;
-  if (tm * tn > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-  a.M = A.rows;
-  a.N = B.rows;
-  a.kblocks = (int)(((long long)A.red + G_BK - 1) / G_BK);
-  a.tiles_m = (int)tm;
-  a.tiles_n = (int)tn;
-  a.num_tiles = (int)(tm * tn);
-  const int grid = a.num_tiles < num_sms() ? a.num_tiles : num_sms();
-  gemm16_kernel<BN, A_MN, B_MN><<<grid, G_THREADS, L::ALLOC, st>>>(ta, tb, a);
-  return cudaGetLastError();
+// ---- which kernel, tile width and split -------------------------------
+// The launch takes the form whose time a small model puts lowest.  In it, a
+// worker (a CTA pair, or a CTA) takes `step` us per stage of 64 reduction
+// elements and `tile` us more per tile, and a launch takes `launch` us; the
+// worker that has the first tile has the most of them.  The constants are
+// fitted to measured launches (us, model / measured):
+//   pair 256   4096 x 1152 to 4608          35 / 35    both gradients  75 / 75
+//   pair 192   4096 x 1152 to 1152          20 / 21    777 x 1152 to 2304  15 / 16
+//   pair 128   4096 x 1152 to 1152          17 / 18    both gradients of 777  21 / 22
+//   split 128  777 x 1152 to 2304           13 / 13    128 x 12288 to 1152 by 8  16 / 16
+//   split 64   333 x 1152 to 2304           10 / 10    1024 x 1152 to 1152  10 / 10
+// The choice matters where the forms differ: 128 x 12288 to 1152 takes 16 us
+// split by 8 and 67 on pairs, 4608 x 12288 to 4608 takes 370 us on pairs and
+// 600 on single CTAs.
+struct G16Choice {
+  bool pair;
+  int bn, splits;
+  double us;
+};
+
+double model_us(const G16Launch& l, int bm, int bn, int splits, int workers, double launch, double tile,
+                double step) {
+  long long tiles[2] = {0, 0};
+  int kb[2] = {0, 0};
+  for (int i = 0; i < 2; ++i)
+    if (l.A[i].p) {
+      tiles[i] = (((long long)l.A[i].rows + bm - 1) / bm) * (((long long)l.B[i].rows + bn - 1) / bn);
+      kb[i] = (int)(((long long)l.A[i].red + G_BK - 1) / G_BK);
+    }
+  // the first worker's tiles of each problem, workers apart
+  const long long n0 = (tiles[0] + workers - 1) / workers;
+  const long long all = (tiles[0] + tiles[1] + workers - 1) / workers;
+  const long long n1 = all - n0;
+  auto part = [&](long long n, int k) { return n * (((k + splits - 1) / splits) * step + tile); };
+  return launch + part(n0, kb[0]) + part(n1, kb[1]);
 }
 
-cudaError_t launch_gemm(const Operand& A, const Operand& B, G16Args a, cudaStream_t st) {
-  a.err = op_err_address();
-  if (!a.err) return cudaErrorInvalidDevice;
-  if (A.rows > 256) return launch_gemm16_pair(A, B, a, st);
-  if (A.mn) return launch_gemm_bn<128, true, true>(A, B, a, st);
-  if (B.mn) return launch_gemm_bn<128, false, true>(A, B, a, st);
-  return launch_gemm_bn<128, false, false>(A, B, a, st);
+G16Choice choose_gemm16(const G16Launch& l) {
+  const bool grad = l.kind == G16Kind::Gradients;
+  const int sms = num_sms();
+  G16Choice best{true, 256, 1, 1e30};
+  auto offer = [&](bool pair, int bn, int splits, double us) {
+    if (us < best.us) best = {pair, bn, splits, us};
+  };
+  offer(true, 256, 1, model_us(l, 256, 256, 1, sms / 2, 10.5, 0.8, 0.30));
+  if (!grad) offer(true, 192, 1, model_us(l, 256, 192, 1, sms / 2, 9.5, 0.7, 0.26));
+  offer(true, 128, 1, model_us(l, 256, 128, 1, sms / 2, 8.0, 0.7, 0.24));
+  int kb = 1 << 30, rows = 128;
+  for (int i = 0; i < 2; ++i)
+    if (l.A[i].p) {
+      const int k = (int)(((long long)l.A[i].red + G_BK - 1) / G_BK);
+      if (k < kb) kb = k;
+      if (!l.A[i].mn && l.A[i].rows < rows) rows = l.A[i].rows;
+    }
+  for (int bn = 128; bn >= (grad ? 64 : 32); bn >>= 1)
+    for (int s = 1; s <= 8 && s <= kb && bn / s >= 8; s <<= 1) {
+      // clusters of 4 and 8 do not fill every SM
+      const int ctas = s == 8 ? sms - 20 : s == 4 ? sms - 4 : sms;
+      const double step = 0.05 + 0.25 * (rows + bn) / 256.0;
+      offer(false, bn, s, model_us(l, 128, bn, s, ctas / s, 1.5 + bn / 85.0, 3.0 + bn / 85.0 + (s > 1 ? 1.5 : 0.0), step));
+    }
+  return best;
+}
+
+cudaError_t launch_gemm(G16Launch& l, cudaStream_t st) {
+  l.err = op_err_address();
+  if (!l.err) return cudaErrorInvalidDevice;
+  const G16Choice c = choose_gemm16(l);
+  return c.pair ? launch_gemm16_pair(l, c.bn, st) : launch_gemm16_split(l, c.bn, c.splits, st);
 }
 
 // Workspace of the backward call: dP, then the column sums' partials.
@@ -419,16 +240,20 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
       (bias && !svdq::is_aligned16(bias)) || (R && !rows_aligned16(R, ldr, 2)) ||
       (P && !rows_aligned16(P, ldp, 2)))
     return SVDQ_ERR_ALIGNMENT;
-  svdq::G16Args a{};
-  a.bias = static_cast<const uint16_t*>(bias);
-  a.res = static_cast<const uint16_t*>(R);
-  a.out = static_cast<uint16_t*>(Y);
-  a.pre = static_cast<uint16_t*>(P);
-  a.ldr = ldr; a.ldo = ldy; a.ldp = ldp;
-  a.epilogue = epilogue;
-  a.bf16 = dtype == SVDQ_DTYPE_BF16;
-  const svdq::Operand A{X, ldx, M, K, false}, B{W, ldw, N, K, false};
-  return svdq::launch_gemm(A, B, a, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  svdq::G16Launch l{};
+  l.kind = svdq::G16Kind::Forward;
+  l.bf16 = dtype == SVDQ_DTYPE_BF16;
+  l.A[0] = {X, ldx, M, K, false};
+  l.B[0] = {W, ldw, N, K, false};
+  svdq::G16Out& o = l.o[0];
+  o.bias = static_cast<const uint16_t*>(bias);
+  o.res = static_cast<const uint16_t*>(R);
+  o.out = static_cast<uint16_t*>(Y);
+  o.pre = static_cast<uint16_t*>(P);
+  o.ldr = ldr; o.ldo = ldy; o.ldp = ldp;
+  o.epilogue = epilogue;
+  o.bf16 = l.bf16;
+  return svdq::launch_gemm(l, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
 }
 
 size_t svdq_linear16_backward_workspace(int M, int K, int N, int epilogue) {
@@ -494,21 +319,20 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
       if (cudaGetLastError() != cudaSuccess) return SVDQ_ERR_CUDA;
     }
   }
-  svdq::G16Args a{};
-  a.epilogue = SVDQ_EPI_NONE;
-  a.bf16 = bf16;
-  if (dX) {
-    a.out = static_cast<uint16_t*>(dX);
-    a.ldo = lddx;
-    const svdq::Operand A{dP, lddp, M, N, false}, B{W, ldw, K, N, true};
-    if (svdq::launch_gemm(A, B, a, stream) != cudaSuccess) return SVDQ_ERR_CUDA;
-  }
-  if (dW) {
-    a.out = static_cast<uint16_t*>(dW);
-    a.ldo = lddw;
-    const svdq::Operand A{dP, lddp, N, M, true}, B{X, ldx, K, M, true};
-    if (svdq::launch_gemm(A, B, a, stream) != cudaSuccess) return SVDQ_ERR_CUDA;
-  }
+  svdq::G16Launch l{};
+  l.kind = svdq::G16Kind::Gradients;
+  l.bf16 = bf16;
+  auto set = [&](int i, const svdq::Operand& A, const svdq::Operand& B, void* out, int ld) {
+    l.A[i] = A;
+    l.B[i] = B;
+    l.o[i].out = static_cast<uint16_t*>(out);
+    l.o[i].ldo = ld;
+    l.o[i].epilogue = SVDQ_EPI_NONE;
+    l.o[i].bf16 = bf16;
+  };
+  if (dX) set(0, {dP, lddp, M, N, false}, {W, ldw, K, N, true}, dX, lddx);
+  if (dW) set(1, {dP, lddp, N, M, true}, {X, ldx, K, M, true}, dW, lddw);
+  if ((dX || dW) && svdq::launch_gemm(l, stream) != cudaSuccess) return SVDQ_ERR_CUDA;
   return SVDQ_OK;
 }
 
