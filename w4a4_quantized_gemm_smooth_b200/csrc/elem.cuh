@@ -106,6 +106,13 @@ __device__ __forceinline__ void store_vec(T* row, int c, int n, const RowVec<T, 
   }
 }
 
+// The kernel after this one in the stream may be brought up; and: everything
+// before this kernel is done and visible (see launch_op).
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ float2 splat2(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ float warp_sum(float v) {

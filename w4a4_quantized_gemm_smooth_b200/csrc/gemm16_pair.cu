@@ -15,6 +15,7 @@
 //   warps 4-11   epilogue: warp w owns TMEM lanes 32 (w % 4).. and one half
 //                of the columns, in boxes of 32 x 32 that leave by TMA.  The
 //                residual's boxes come by TMA into the same place before.
+#include "elem.cuh"
 #include "gemm16.cuh"
 
 namespace svdq {
@@ -72,7 +73,7 @@ __device__ __forceinline__ void commit_pair(uint32_t mbar) {
 }
 
 template <int BN, bool GRAD>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+__global__ void __launch_bounds__(P_THREADS, 1)
 gemm16_pair_kernel(const __grid_constant__ G16Problem p0, const __grid_constant__ G16Problem p1,
                    const int total, const int bf16, int* err) {
   using L = PLay<BN>;
@@ -116,6 +117,7 @@ gemm16_pair_kernel(const __grid_constant__ G16Problem p0, const __grid_constant_
   __syncthreads();
   cluster_sync();                 // the peer's barriers are ready
   tc_fence_after();
+  grid_wait();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
@@ -312,8 +314,8 @@ cudaError_t launch_bn(const G16Launch& l, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int total = p[0].tiles + p[1].tiles;
   const int pairs = total < num_sms() / 2 ? total : num_sms() / 2;
-  gemm16_pair_kernel<BN, GRAD><<<2 * pairs, P_THREADS, L::ALLOC, st>>>(p[0], p[1], total, l.bf16, l.err);
-  return cudaGetLastError();
+  return launch_op(gemm16_pair_kernel<BN, GRAD>, dim3(2 * pairs), P_THREADS, L::ALLOC, 2, st, p[0], p[1],
+                   total, l.bf16, l.err);
 }
 
 }  // namespace

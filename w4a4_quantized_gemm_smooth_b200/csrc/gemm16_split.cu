@@ -10,6 +10,7 @@
 // epilogue on it.  No workspace, no atomics, one launch.
 //
 // 10 warps: TMA, MMA (and TMEM), eight epilogue warps.
+#include "elem.cuh"
 #include "gemm16.cuh"
 
 namespace svdq {
@@ -89,6 +90,7 @@ gemm16_split_kernel(const __grid_constant__ G16Problem p0, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_wait();
   const uint32_t tmem = *tmem_slot;
 
   const int w = warp - S_EPI0, q = warp & 3, half = w >> 2;
@@ -248,18 +250,8 @@ cudaError_t launch_bn(const G16Launch& l, int splits, cudaStream_t st) {
         return make_problem(q, A, B, o, 128, BN, 128, BN, splits == 1);
       }))
     return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p[0].tiles + p[1].tiles) * splits));
-  cfg.blockDim = dim3(S_THREADS);
-  cfg.dynamicSmemBytes = L::ALLOC;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)splits;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm16_split_kernel<BN, GRAD>, p[0], p[1], splits, l.bf16, l.err);
+  return launch_op(gemm16_split_kernel<BN, GRAD>, dim3((unsigned)((p[0].tiles + p[1].tiles) * splits)),
+                   S_THREADS, L::ALLOC, splits, st, p[0], p[1], splits, l.bf16, l.err);
 }
 
 }  // namespace

@@ -67,10 +67,11 @@ struct NormCfg {
   static constexpr bool PSMEM = G < 512;
   static constexpr int RF = G < 512 ? 2 : 1;                   // rows at a time, forward
   static constexpr int DF = 2;                                 // and steps in flight
-  static constexpr int DB = NV < 8 ? 2 : 1;                    // backward (x and dy)
+  static constexpr int RB = G < 512 ? 2 : 1;                   // backward (x and dy): rows at a time
+  static constexpr int DB = NV < 8 ? 2 : 1;                    // and steps in flight
   static constexpr size_t PARAM = PSMEM ? (size_t)NV * G * V * 4 : 0;   // one fp32 row
   static constexpr size_t RING_FWD = (size_t)DF * RF * NV * THREADS * 16;
-  static constexpr size_t RING_BWD = (size_t)DB * 2 * NV * THREADS * 16;
+  static constexpr size_t RING_BWD = (size_t)DB * RB * 2 * NV * THREADS * 16;
   static constexpr size_t FWD_SMEM = RING_FWD + 2 * PARAM;
   static constexpr size_t BWD_SMEM = RING_BWD + PARAM;
   static_assert(FWD_SMEM <= 227 * 1024 && BWD_SMEM <= 227 * 1024, "shared memory");
@@ -96,6 +97,11 @@ struct RowShare {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                    ::"r"(dst + i * pitch), "l"(src), "r"(i + 1 < NV ? 16 : last) : "memory");
     }
+  }
+  // A row of zeros in the same place.
+  __device__ __forceinline__ void clear(uint4* dst, uint32_t pitch) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) dst[i * pitch] = make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -186,6 +192,7 @@ norm_kernel(const NormArgs p) {
   extern __shared__ uint4 smem[];
   __shared__ float red[2 * R * (G > 32 ? G / 32 : 1)];
   const int lane = threadIdx.x % G, team = threadIdx.x / G;
+  grid_wait();
   const RowSpan span = block_span(p.M, p.rows_per_group, p.splits);
   const T* x = static_cast<const T*>(p.x);
   const uint4* ring = smem + threadIdx.x;              // vector (slot, row, i) at ((slot R + row) NV + i) TH
@@ -303,6 +310,9 @@ norm_kernel(const NormArgs p) {
   }
 }
 
+// Floats of a partial row.
+__host__ __device__ constexpr int part_pitch(int K) { return (K + 7) / 8 * 8; }
+
 struct NormBwdArgs {
   const void* dy;
   const void* x;
@@ -312,7 +322,7 @@ struct NormBwdArgs {
   void* dx;
   void* dw;
   void* db;
-  float* part;               // [blocks][2][K] when split, unused otherwise
+  float* part;               // [blocks][2][part_pitch(K)] when split, unused otherwise
   long long lddy, ldx, ldw, lddx, lddw, lddb;
   int M, K, rows_per_group;  // rows_per_group >= 1 here
   int splits;                // blocks per group
@@ -321,17 +331,18 @@ struct NormBwdArgs {
 
 // PARAMS: dweight or dbias is wanted.
 template <typename T, typename PT, int G, int NV, bool PARAMS>
-__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 3 : 1)
+__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 2 : 1)
 norm_bwd_kernel(const NormBwdArgs p) {
   using C = NormCfg<T, G, NV>;
-  constexpr int V = C::V, H = C::H, D = C::DB, TH = C::THREADS, TEAMS = C::TEAMS;
+  constexpr int V = C::V, H = C::H, D = C::DB, TH = C::THREADS, TEAMS = C::TEAMS, R = C::RB;
   extern __shared__ uint4 smem[];
-  __shared__ float red[2 * (G > 32 ? 2 * (G / 32) : 1)];
+  __shared__ float red[2 * (G > 32 ? 2 * R * (G / 32) : 1)];
   const int lane = threadIdx.x % G, team = threadIdx.x / G;
+  grid_wait();
   const RowSpan span = block_span(p.M, p.rows_per_group, p.splits);
   const T* x = static_cast<const T*>(p.x);
   const T* dy = static_cast<const T*>(p.dy);
-  const uint4* ring = smem + threadIdx.x;    // slot: NV vectors of x, then NV of dy
+  uint4* ring = smem + threadIdx.x;          // (slot, row): NV vectors of x, then NV of dy
   const uint32_t ring_u = smem_u32(ring);
   float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_BWD);
   const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
@@ -339,20 +350,33 @@ norm_bwd_kernel(const NormBwdArgs p) {
   ParamStage<PT, V, G, C::PSMEM ? NV : 1, TH> sw;
   if constexpr (C::PSMEM)
     if (w) sw.load(w, p.K);
-  float nmu[D], nrs[D];                      // the statistics of the rows in flight
+  float nmu[D][R], nrs[D][R];                // the statistics of the rows in flight
   auto fetch = [&](long long row, int slot) {
-    if (row < span.r1) {
-      share.fetch(x + row * p.ldx, lane, ring_u + slot * 2 * NV * TH * 16, TH * 16);
-      share.fetch(dy + row * p.lddy, lane, ring_u + (slot * 2 + 1) * NV * TH * 16, TH * 16);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int at = (slot * R + k) * 2 * NV * TH;
+      if (row + k < span.r1) {
+        share.fetch(x + (row + k) * p.ldx, lane, ring_u + at * 16, TH * 16);
+        share.fetch(dy + (row + k) * p.lddy, lane, ring_u + (at + NV * TH) * 16, TH * 16);
+      } else if (k > 0 && row < span.r1) {   // a step's missing row adds nothing
+        share.clear(ring + at, TH);
+        share.clear(ring + at + NV * TH, TH);
+      }
     }
     cp_async_commit();
   };
+  auto stats = [&](long long row, float (&mu)[R], float (&rs)[R]) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      mu[k] = row + k < span.r1 ? p.mean[row + k] : 0.0f;
+      rs[k] = row + k < span.r1 ? p.rstd[row + k] : 0.0f;
+    }
+  };
 #pragma unroll
   for (int d = 0; d < D; ++d) {
-    const long long row = span.r0 + team + d * TEAMS;
+    const long long row = span.r0 + (team + d * TEAMS) * R;
     fetch(row, d);
-    nmu[d] = row < span.r1 ? p.mean[row] : 0.0f;
-    nrs[d] = row < span.r1 ? p.rstd[row] : 0.0f;
+    stats(row, nmu[d], nrs[d]);
   }
   const float inv_k = 1.0f / (float)p.K;
   float2 aw[PARAMS ? NV : 1][H], ab[PARAMS ? NV : 1][H];
@@ -367,80 +391,88 @@ norm_bwd_kernel(const NormBwdArgs p) {
     __syncthreads();
   }
   int slot = 0, phase = 0;
-  for (long long row = span.r0 + team; row < span.r1; row += TEAMS) {
+  // R rows at a time: their sums overlap, and the scale is read once
+  for (long long row = span.r0 + team * R; row < span.r1; row += TEAMS * R) {
     cp_async_wait<D - 1>();
-    const uint4* q = ring + slot * 2 * NV * TH;
-    const float2 m = splat2(-nmu[0]), r = splat2(nrs[0]);
-    // the statistics of the row D further on, long before they are needed
-    const long long ahead = row + (long long)D * TEAMS;
+    const uint4* q = ring + slot * R * 2 * NV * TH;
+    float2 m[R], r[R], s1[R], s2[R];
 #pragma unroll
-    for (int d = 0; d + 1 < D; ++d) {
-      nmu[d] = nmu[d + 1];
-      nrs[d] = nrs[d + 1];
+    for (int k = 0; k < R; ++k) {
+      m[k] = splat2(-nmu[0][k]);
+      r[k] = splat2(nrs[0][k]);
+      s1[k] = s2[k] = make_float2(0.0f, 0.0f);
     }
-    if (ahead < span.r1) {
-      nmu[D - 1] = p.mean[ahead];
-      nrs[D - 1] = p.rstd[ahead];
-    }
-    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+    // the statistics of the rows D steps on, long before they are needed
+    const long long ahead = row + (long long)D * TEAMS * R;
+#pragma unroll
+    for (int d = 0; d + 1 < D; ++d)
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        nmu[d][k] = nmu[d + 1][k];
+        nrs[d][k] = nrs[d + 1][k];
+      }
+    stats(ahead, nmu[D - 1], nrs[D - 1]);
     // columns past K: x and dy read as 0 and add 0 to every sum
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const RowVec<T, V> xr = read_vec<T, V>(q + i * TH, TH), dr = read_vec<T, V>(q + (NV + i) * TH, TH);
       float2 f[H];
       if (w) read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
 #pragma unroll
-      for (int j = 0; j < H; ++j) {
-        const float2 d = dr.get(j);
-        const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m), r);
-        if constexpr (PARAMS) {
-          aw[i][j] = __ffma2_rn(d, h, aw[i][j]);
-          ab[i][j] = __fadd2_rn(ab[i][j], d);
+      for (int k = 0; k < R; ++k) {
+        const RowVec<T, V> xr = read_vec<T, V>(q + (2 * k * NV + i) * TH, TH);
+        const RowVec<T, V> dr = read_vec<T, V>(q + ((2 * k + 1) * NV + i) * TH, TH);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const float2 d = dr.get(j);
+          const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m[k]), r[k]);
+          if constexpr (PARAMS) {
+            aw[i][j] = __ffma2_rn(d, h, aw[i][j]);
+            ab[i][j] = __fadd2_rn(ab[i][j], d);
+          }
+          const float2 t = w ? __fmul2_rn(d, f[j]) : d;
+          s1[k] = __fadd2_rn(s1[k], t);
+          s2[k] = __ffma2_rn(t, h, s2[k]);
         }
-        const float2 t = w ? __fmul2_rn(d, f[j]) : d;
-        s1 = __fadd2_rn(s1, t);
-        s2 = __ffma2_rn(t, h, s2);
       }
     }
     if (p.dx) {
-      float a1 = warp_sum(s1.x + s1.y), a2 = warp_sum(s2.x + s2.y);
-      if constexpr (G > 32) {
-        constexpr int W = G / 32;
-        float* rd = red + phase * 2 * W;    // two buffers: one barrier per row
-        if ((threadIdx.x & 31) == 0) {
-          rd[threadIdx.x >> 5] = a1;
-          rd[W + (threadIdx.x >> 5)] = a2;
-        }
-        __syncthreads();
-        a1 = a2 = 0.0f;
+      float sum[2 * R];
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          a1 += rd[i];
-          a2 += rd[W + i];
-        }
-        phase ^= 1;
+      for (int k = 0; k < R; ++k) {
+        sum[2 * k] = s1[k].x + s1[k].y;
+        sum[2 * k + 1] = s2[k].x + s2[k].y;
       }
-      // read the row again rather than hold it: its registers would halve the
-      // blocks on an SM
+      team_sum<G, 2 * R>(sum, red + phase * (G > 32 ? 2 * R * (G / 32) : 0));
+      phase ^= 1;
+      // read the rows again rather than hold them: the registers are few
       asm volatile("" ::: "memory");
-      const float2 n1 = splat2(-a1 * inv_k), n2 = splat2(-a2 * inv_k);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        s1[k] = splat2(-sum[2 * k] * inv_k);
+        s2[k] = splat2(-sum[2 * k + 1] * inv_k);
+      }
       T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (lane + i * G) * V;
         if (i + 1 < NV || c < p.K) {
-          const RowVec<T, V> xr = read_vec<T, V>(q + i * TH, TH), dr = read_vec<T, V>(q + (NV + i) * TH, TH);
           float2 f[H];
           if (w) read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
-          RowVec<T, V> o;
 #pragma unroll
-          for (int j = 0; j < H; ++j) {
-            const float2 d = dr.get(j);
-            const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m), r);
-            const float2 t = w ? __fmul2_rn(d, f[j]) : d;
-            o.set(j, __fmul2_rn(r, __ffma2_rn(h, n2, __fadd2_rn(t, n1))));
+          for (int k = 0; k < R; ++k) {
+            const RowVec<T, V> xr = read_vec<T, V>(q + (2 * k * NV + i) * TH, TH);
+            const RowVec<T, V> dr = read_vec<T, V>(q + ((2 * k + 1) * NV + i) * TH, TH);
+            RowVec<T, V> o;
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+              const float2 d = dr.get(j);
+              const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m[k]), r[k]);
+              const float2 t = w ? __fmul2_rn(d, f[j]) : d;
+              o.set(j, __fmul2_rn(r[k], __ffma2_rn(h, s2[k], __fadd2_rn(t, s1[k]))));
+            }
+            if (k == 0 || row + k < span.r1)
+              store_vec<T, V>(dx + k * p.lddx, c, i + 1 < NV ? INT_MAX : p.K, o);
           }
-          store_vec<T, V>(dx, c, i + 1 < NV ? INT_MAX : p.K, o);
         }
       }
     }
@@ -480,7 +512,8 @@ norm_bwd_kernel(const NormBwdArgs p) {
     // an own row of the gradients, or this block's partial row
     PT* dw = whole && p.dw ? static_cast<PT*>(p.dw) + span.g * p.lddw : nullptr;
     PT* db = whole && p.db ? static_cast<PT*>(p.db) + span.g * p.lddb : nullptr;
-    float* part = p.part + (whole ? 0 : (size_t)blockIdx.x * 2 * p.K);
+    // partial rows of K rounded up to 8 elements: whole vectors
+    float* part = p.part + (whole ? 0 : (size_t)blockIdx.x * 2 * part_pitch(p.K));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * G) * V;
@@ -495,16 +528,12 @@ norm_bwd_kernel(const NormBwdArgs p) {
         if (dw) store_vec<PT, V>(dw, c, p.K, ow);
         if (db) store_vec<PT, V>(db, c, p.K, ob);
       } else {
+        float4* dst_w = reinterpret_cast<float4*>(part + c);
+        float4* dst_b = reinterpret_cast<float4*>(part + part_pitch(p.K) + c);
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-          if (c + 2 * j < p.K) {
-            part[c + 2 * j] = aw[i][j].x;
-            part[p.K + c + 2 * j] = ab[i][j].x;
-          }
-          if (c + 2 * j + 1 < p.K) {
-            part[c + 2 * j + 1] = aw[i][j].y;
-            part[p.K + c + 2 * j + 1] = ab[i][j].y;
-          }
+        for (int j = 0; j < H; j += 2) {
+          dst_w[j / 2] = make_float4(aw[i][j].x, aw[i][j].y, aw[i][j + 1].x, aw[i][j + 1].y);
+          dst_b[j / 2] = make_float4(ab[i][j].x, ab[i][j].y, ab[i][j + 1].x, ab[i][j + 1].y);
         }
       }
     }
@@ -519,6 +548,7 @@ __global__ void __launch_bounds__(256)
 norm_bwd_join_kernel(const float* part, int splits, int K, PT* dw, long long lddw, PT* db,
                      long long lddb) {
   __shared__ float sh[8][33];
+  grid_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   const int which = blockIdx.y & 1;
@@ -526,9 +556,10 @@ norm_bwd_join_kernel(const float* part, int splits, int K, PT* dw, long long ldd
   float acc = 0.0f;
   if (c < K) {
     const int s0 = splits * ty / 8, s1 = splits * (ty + 1) / 8;
-    const float* q = part + ((size_t)g * splits + s0) * 2 * K + (size_t)which * K + c;
+    const size_t pitch = part_pitch(K);
+    const float* q = part + (((size_t)g * splits + s0) * 2 + which) * pitch + c;
 #pragma unroll 8
-    for (int s = s0; s < s1; ++s, q += 2 * (size_t)K) acc += *q;
+    for (int s = s0; s < s1; ++s, q += 2 * pitch) acc += *q;
   }
   sh[ty][tx] = acc;
   __syncthreads();
@@ -552,7 +583,7 @@ int split_rows(int M, int rows_per_group, int per_sm, int rows) {
 }
 // Backward: at least eight rows per block (two per warp of a four-warp
 // block), so that the partial sums stay a small share of the traffic.
-int bwd_splits(int M, int rows_per_group) { return split_rows(M, rows_per_group, 3, 8); }
+int bwd_splits(int M, int rows_per_group) { return split_rows(M, rows_per_group, 2, 8); }
 
 // Raises the kernel's dynamic shared-memory limit once per device.
 template <typename K>
@@ -574,8 +605,8 @@ cudaError_t fwd_launch(NormArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long groups = ((long long)a.M + a.rows_per_group - 1) / a.rows_per_group;
   a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : 4, C::TEAMS);
-  norm_kernel<T, PT, G, NV><<<(unsigned)(groups * a.splits), C::THREADS, C::FWD_SMEM, st>>>(a);
-  return cudaGetLastError();
+  return launch_op(norm_kernel<T, PT, G, NV>, dim3((unsigned)(groups * a.splits)), C::THREADS,
+                   C::FWD_SMEM, 1, st, a);
 }
 
 // Team and vectors per thread for a row of `vecs` 16-byte vectors of V
@@ -621,13 +652,12 @@ cudaError_t bwd_launch(const NormBwdArgs& a, long long groups, cudaStream_t st) 
   if (a.dw || a.db) {
     e = allow_smem(norm_bwd_kernel<T, PT, G, NV, true>, C::BWD_SMEM, done[0]);
     if (e != cudaSuccess) return e;
-    norm_bwd_kernel<T, PT, G, NV, true><<<blocks, C::THREADS, C::BWD_SMEM, st>>>(a);
+    return launch_op(norm_bwd_kernel<T, PT, G, NV, true>, dim3(blocks), C::THREADS, C::BWD_SMEM, 1, st, a);
   } else {
     e = allow_smem(norm_bwd_kernel<T, PT, G, NV, false>, C::BWD_SMEM, done[1]);
     if (e != cudaSuccess) return e;
-    norm_bwd_kernel<T, PT, G, NV, false><<<blocks, C::THREADS, C::BWD_SMEM, st>>>(a);
+    return launch_op(norm_bwd_kernel<T, PT, G, NV, false>, dim3(blocks), C::THREADS, C::BWD_SMEM, 1, st, a);
   }
-  return cudaGetLastError();
 }
 
 template <typename T, typename PT>
@@ -639,9 +669,8 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t st) {
   });
   if (e != cudaSuccess || a.splits == 1 || (!a.dw && !a.db)) return e;
   const dim3 grid((unsigned)((a.K + 31) / 32), 2, (unsigned)groups);
-  norm_bwd_join_kernel<PT><<<grid, 256, 0, st>>>(a.part, a.splits, a.K, static_cast<PT*>(a.dw),
-                                                 a.lddw, static_cast<PT*>(a.db), a.lddb);
-  return cudaGetLastError();
+  return launch_op(norm_bwd_join_kernel<PT>, grid, 256, 0, 1, st, a.part, a.splits, a.K,
+                   static_cast<PT*>(a.dw), a.lddw, static_cast<PT*>(a.db), a.lddb);
 }
 
 // f(T{}, PT{}) for the element and parameter types.
@@ -701,7 +730,7 @@ size_t svdq_layer_norm_backward_workspace(int M, int K, int rows_per_group) {
   const int rpg = rows_per_group ? rows_per_group : M;
   const size_t groups = ((size_t)M + rpg - 1) / rpg;
   const int s = svdq::bwd_splits(M, rpg);
-  return s == 1 ? 0 : groups * s * 2 * (size_t)K * sizeof(float);
+  return s == 1 ? 0 : groups * s * 2 * (size_t)svdq::part_pitch(K) * sizeof(float);
 }
 
 svdq_status svdq_layer_norm_backward(int dtype, int param_dtype, int M, int K, const void* dY,

@@ -39,48 +39,54 @@ struct DpArgs {
   float* part;             // [row blocks][N8] column sums, or null
   long long lddy, ldp, lddp;
   int M, N, rows_per_block;
-  int epilogue, bf16;
+  int bf16;
 };
 
 // 32 columns x 8 per thread by 8 rows of threads.
-constexpr int DP_COLS = 256;
+constexpr int DP_COLS = 256, DP_ROWS = 4;
+template <int EPI>
 __global__ void __launch_bounds__(256)
 dp_kernel(const DpArgs a) {
+  grid_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * DP_COLS + tx * 8;
   const bool bf16 = a.bf16 != 0;
   const long long r0 = (long long)blockIdx.y * a.rows_per_block;
   const long long r1 = min((long long)a.M, r0 + a.rows_per_block);
-  float acc[8] = {};
+  float2 acc[4] = {};
   if (c < a.N) {
-    for (long long r = r0 + ty; r < r1; r += 8) {
-      const uint4 d4 = load8(a.dy + r * a.lddy, c, a.N);
-      uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
-      if (a.p) {
-        const uint4 p4 = load8(a.p + r * a.ldp, c, a.N);
-        const uint32_t pw[4] = {p4.x, p4.y, p4.z, p4.w};
+    // DP_ROWS rows at a time, so that their loads are in flight together
+    for (long long r = r0 + ty; r < r1; r += 8 * DP_ROWS) {
+      uint4 d4[DP_ROWS], p4[DP_ROWS];
+#pragma unroll
+      for (int k = 0; k < DP_ROWS; ++k) {
+        const bool in = r + 8 * k < r1;
+        d4[k] = in ? load8(a.dy + (r + 8 * k) * a.lddy, c, a.N) : make_uint4(0, 0, 0, 0);
+        p4[k] = in && a.p ? load8(a.p + (r + 8 * k) * a.ldp, c, a.N) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < DP_ROWS; ++k) {
+        uint32_t dw[4] = {d4[k].x, d4[k].y, d4[k].z, d4[k].w};
+        const uint32_t pw[4] = {p4[k].x, p4[k].y, p4[k].z, p4[k].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 d = __fmul2_rn(unpack2(dw[e], bf16), g_act_grad2(unpack2(pw[e], bf16), a.epilogue));
-          acc[2 * e] += d.x;
-          acc[2 * e + 1] += d.y;
+          float2 d = unpack2(dw[e], bf16);
+          if (EPI != SVDQ_EPI_NONE) d = __fmul2_rn(d, g_act_grad2(unpack2(pw[e], bf16), EPI));
+          acc[e] = __fadd2_rn(acc[e], d);
           dw[e] = pack2(d, bf16);
         }
-        store8(a.dp + r * a.lddp, c, a.N, make_uint4(dw[0], dw[1], dw[2], dw[3]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 d = unpack2(dw[e], bf16);
-          acc[2 * e] += d.x;
-          acc[2 * e + 1] += d.y;
-        }
+        if (EPI != SVDQ_EPI_NONE && r + 8 * k < r1)
+          store8(a.dp + (r + 8 * k) * a.lddp, c, a.N, make_uint4(dw[0], dw[1], dw[2], dw[3]));
       }
     }
   }
   if (!a.part) return;
   __shared__ float sh[8][DP_COLS + 8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sh[ty][tx * 8 + e] = acc[e];
+  for (int e = 0; e < 4; ++e) {
+    sh[ty][tx * 8 + 2 * e] = acc[e].x;
+    sh[ty][tx * 8 + 2 * e + 1] = acc[e].y;
+  }
   __syncthreads();
   const int col = blockIdx.x * DP_COLS + threadIdx.x;
   if (col < a.N) {
@@ -95,6 +101,7 @@ dp_kernel(const DpArgs a) {
 __global__ void __launch_bounds__(256)
 db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
   __shared__ float sh[8][33];
+  grid_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   float acc = 0.0f;
@@ -297,7 +304,7 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
     svdq::DpArgs d{};
     d.dy = static_cast<const uint16_t*>(dY);
     d.lddy = lddy;
-    d.M = M; d.N = N; d.epilogue = epilogue; d.bf16 = bf16;
+    d.M = M; d.N = N; d.bf16 = bf16;
     if (act) {
       d.p = static_cast<const uint16_t*>(P);
       d.ldp = ldp;
@@ -311,13 +318,14 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
     d.rows_per_block = (int)(((long long)M + want - 1) / want);
     const int blocks = (int)(((long long)M + d.rows_per_block - 1) / d.rows_per_block);
     const dim3 grid((unsigned)(((long long)N + svdq::DP_COLS - 1) / svdq::DP_COLS), (unsigned)blocks);
-    svdq::dp_kernel<<<grid, 256, 0, stream>>>(d);
-    if (cudaGetLastError() != cudaSuccess) return SVDQ_ERR_CUDA;
-    if (db) {
-      svdq::db_join_kernel<<<(unsigned)(((long long)N + 31) / 32), 256, 0, stream>>>(
-          d.part, blocks, N, static_cast<uint16_t*>(db), bf16);
-      if (cudaGetLastError() != cudaSuccess) return SVDQ_ERR_CUDA;
-    }
+    auto kernel = epilogue == SVDQ_EPI_GELU   ? svdq::dp_kernel<SVDQ_EPI_GELU>
+                  : epilogue == SVDQ_EPI_SILU ? svdq::dp_kernel<SVDQ_EPI_SILU>
+                                              : svdq::dp_kernel<SVDQ_EPI_NONE>;
+    if (svdq::launch_op(kernel, grid, 256, 0, 1, stream, d) != cudaSuccess) return SVDQ_ERR_CUDA;
+    if (db && svdq::launch_op(svdq::db_join_kernel, dim3((unsigned)(((long long)N + 31) / 32)), 256, 0,
+                              1, stream, d.part, blocks, N, static_cast<uint16_t*>(db),
+                              bf16) != cudaSuccess)
+      return SVDQ_ERR_CUDA;
   }
   svdq::G16Launch l{};
   l.kind = svdq::G16Kind::Gradients;

@@ -8,9 +8,9 @@ namespace svdq {
 
 // Rotary frequencies as fractions of a turn (times 2^64) and each pair's
 // axis; passed to the kernel by value.
-struct RopeTurns {
-  uint64_t turn[SVDQ_ROPE_MAX_PAIRS];
-  uint8_t axis[SVDQ_ROPE_MAX_PAIRS];
+struct alignas(16) RopeTurns {
+  uint64_t turn[SVDQ_ROPE_MAX_PAIRS + 8];     // zeros past the pairs
+  uint8_t axis[SVDQ_ROPE_MAX_PAIRS + 8];
   int pairs, axes;
 };
 
@@ -19,6 +19,30 @@ inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p)
 // Rows of `ld` elements of `esize` bytes start on 16-byte boundaries.
 inline bool rows_aligned16(const void* p, int ld, int esize) {
   return is_aligned16(p) && ((long long)ld * esize) % 16 == 0;
+}
+
+// Launch of a 16-bit operator's kernel: it may start while the kernel before
+// it in the stream runs out (its blocks then set up their shared memory and
+// wait), which hides the launch behind that kernel's last blocks.  Every such
+// kernel calls grid_wait() in all its threads before it touches global
+// memory, so that what it reads and overwrites is in order.
+template <typename... P, typename... A>
+cudaError_t launch_op(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                      cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 inline int dtype_size(int dtype) { return dtype == SVDQ_DTYPE_F32 ? 4 : 2; }

@@ -50,67 +50,124 @@ constexpr int ROPE_BATCH = 4;      // heads whose loads are in flight together
 // V elements per vector.  HALVES: a unit below rot_units holds pairs
 // [V unit, V unit + V) as two vectors P elements apart, a later unit one
 // vector past the pairs; interleaved: a unit is one vector.
+// V elements of a head, of any alignment; pairs of them as fp32.
 template <typename T, int V, int ALIGN>
 struct alignas(ALIGN) RopeVec {
   T e[V];
 };
+__device__ __forceinline__ float2 rope_get(const __nv_bfloat16* e) {
+  return make_float2(__bfloat162float(e[0]), __bfloat162float(e[1]));
+}
+__device__ __forceinline__ float2 rope_get(const __half* e) {
+  return make_float2(__half2float(e[0]), __half2float(e[1]));
+}
+__device__ __forceinline__ float2 rope_get(const float* e) { return make_float2(e[0], e[1]); }
+__device__ __forceinline__ void rope_set(__nv_bfloat16* e, float2 f) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(f);
+  e[0] = h.x;
+  e[1] = h.y;
+}
+__device__ __forceinline__ void rope_set(__half* e, float2 f) {
+  const __half2 h = __float22half2_rn(f);
+  e[0] = h.x;
+  e[1] = h.y;
+}
+__device__ __forceinline__ void rope_set(float* e, float2 f) {
+  e[0] = f.x;
+  e[1] = f.y;
+}
 
+// V elements per vector.  HALVES: a unit below rot_units holds pairs
+// [V unit, V unit + V) as two vectors P elements apart, a later unit one
+// vector past the pairs; interleaved: a unit is one vector.  Arithmetic runs
+// on packed fp32 pairs.
 template <typename T, int V, bool HALVES, int ALIGN>
-__global__ void __launch_bounds__(ROPE_THREADS)
+__global__ void __launch_bounds__(ROPE_THREADS, HALVES && V * (int)sizeof(T) == 16 ? 3 : 5)
 rope_kernel(const __grid_constant__ RopeTurns turns, const RopeArgs p) {
   using VT = RopeVec<T, V, ALIGN>;
+  grid_wait();
   const long long i = (long long)blockIdx.x * ROPE_THREADS + threadIdx.x;
   if (i >= p.work) return;
-  const long long tok = i / p.units;
+  const long long tok = p.work <= 0x7FFFFFFF ? (int)i / p.units : i / p.units;
   const int u = (int)(i - tok * p.units);
   const int h0 = blockIdx.y * p.heads_per_thread;
   const int h1 = min(p.heads, h0 + p.heads_per_thread);
-  const T* x = static_cast<const T*>(p.x) + tok * p.ldxt;
-  T* y = static_cast<T*>(p.y) + tok * p.ldyt;
+  const T* x = static_cast<const T*>(p.x) + tok * p.ldxt + h0 * p.ldxh;
+  T* y = static_cast<T*>(p.y) + tok * p.ldyt + h0 * p.ldyh;
   constexpr int NP = HALVES ? V : V / 2;          // pairs of a unit
   const bool rot = HALVES ? u < p.rot_units : u * NP < p.pairs;
   if (!rot) {
     if (p.in_place) return;
     const int d = HALVES ? 2 * p.pairs + (u - p.rot_units) * V : u * V;
-    for (int h = h0; h < h1; ++h)
-      *reinterpret_cast<VT*>(y + h * p.ldyh + d) = *reinterpret_cast<const VT*>(x + h * p.ldxh + d);
+    for (int h = h0; h < h1; ++h, x += p.ldxh, y += p.ldyh)
+      *reinterpret_cast<VT*>(y + d) = *reinterpret_cast<const VT*>(x + d);
     return;
   }
-  const int32_t* pos = p.pos + (long long)(tok % p.pos_rows) * p.ld_pos;
+  const int32_t* pos = p.pos + (long long)((int)tok % p.pos_rows) * p.ld_pos;
   float c[NP], s[NP];
+  {
+    // the unit's frequencies in one run: lanes read different places of the
+    // parameters, which costs a pass per place, so wide reads are few passes
+    uint64_t turn[NP];
+    uint8_t axis[NP];
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    const int pr = u * NP + j;
-    c[j] = 1.0f;
-    s[j] = 0.0f;
-    if (pr < p.pairs) sincos_turn(pos[turns.axis[pr]], turns.turn[pr], p.inverse != 0, c[j], s[j]);
+    for (int j = 0; j < NP; ++j) {
+      turn[j] = turns.turn[u * NP + j];           // zeros past the pairs
+      axis[j] = turns.axis[u * NP + j];
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) sincos_turn(pos[axis[j]], turn[j], p.inverse != 0, c[j], s[j]);
   }
-  const int d0 = u * V, d1 = d0 + p.pairs;
-  for (int h = h0; h < h1; h += ROPE_BATCH) {
+  x += u * V;
+  y += u * V;
+  const int pairs = p.pairs;
+  // a vector may straddle the last pair: what follows is copied as it is
+  const int live = HALVES ? NP : min(NP, pairs - u * NP);
+  auto turn_head = [&](VT& a, VT& b) {
+    if constexpr (!HALVES) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float2 v = rope_get(&a.e[2 * j]);
+        const float2 r = __ffma2_rn(make_float2(v.y, v.x), make_float2(-s[j], s[j]),
+                                    __fmul2_rn(v, make_float2(c[j], c[j])));
+        if (j < live) rope_set(&a.e[2 * j], r);
+      }
+    } else if constexpr (V == 1) {
+      const float fa = Elem<T>::to_f(a.e[0]), fb = Elem<T>::to_f(b.e[0]);
+      a.e[0] = Elem<T>::from_f(fa * c[0] - fb * s[0]);
+      b.e[0] = Elem<T>::from_f(fa * s[0] + fb * c[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const float2 fa = rope_get(&a.e[j]), fb = rope_get(&b.e[j]);
+        const float2 c2 = make_float2(c[j], c[j + 1]), s2 = make_float2(s[j], s[j + 1]);
+        rope_set(&a.e[j], __ffma2_rn(fb, make_float2(-s2.x, -s2.y), __fmul2_rn(fa, c2)));
+        rope_set(&b.e[j], __ffma2_rn(fa, s2, __fmul2_rn(fb, c2)));
+      }
+    }
+  };
+  const long long ldxh = p.ldxh, ldyh = p.ldyh;
+  int n = h1 - h0;
+  for (; n >= ROPE_BATCH; n -= ROPE_BATCH) {      // a batch's loads are in flight together
     VT a[ROPE_BATCH], b[ROPE_BATCH];
 #pragma unroll
-    for (int k = 0; k < ROPE_BATCH; ++k)
-      if (h + k < h1) {
-        a[k] = *reinterpret_cast<const VT*>(x + (h + k) * p.ldxh + d0);
-        if (HALVES) b[k] = *reinterpret_cast<const VT*>(x + (h + k) * p.ldxh + d1);
-      }
+    for (int k = 0; k < ROPE_BATCH; ++k, x += ldxh) {
+      a[k] = *reinterpret_cast<const VT*>(x);
+      if (HALVES) b[k] = *reinterpret_cast<const VT*>(x + pairs);
+    }
 #pragma unroll
-    for (int k = 0; k < ROPE_BATCH; ++k)
-      if (h + k < h1) {
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          T& ea = HALVES ? a[k].e[j] : a[k].e[2 * j];
-          T& eb = HALVES ? b[k].e[j] : a[k].e[2 * j + 1];
-          // a vector may straddle the last pair: what follows is copied as it is
-          if (HALVES || u * NP + j < p.pairs) {
-            const float fa = Elem<T>::to_f(ea), fb = Elem<T>::to_f(eb);
-            ea = Elem<T>::from_f(fa * c[j] - fb * s[j]);
-            eb = Elem<T>::from_f(fa * s[j] + fb * c[j]);
-          }
-        }
-        *reinterpret_cast<VT*>(y + (h + k) * p.ldyh + d0) = a[k];
-        if (HALVES) *reinterpret_cast<VT*>(y + (h + k) * p.ldyh + d1) = b[k];
-      }
+    for (int k = 0; k < ROPE_BATCH; ++k, y += ldyh) {
+      turn_head(a[k], b[k]);
+      *reinterpret_cast<VT*>(y) = a[k];
+      if (HALVES) *reinterpret_cast<VT*>(y + pairs) = b[k];
+    }
+  }
+  for (; n > 0; --n, x += ldxh, y += ldyh) {
+    VT a = *reinterpret_cast<const VT*>(x), b;
+    if (HALVES) b = *reinterpret_cast<const VT*>(x + pairs);
+    turn_head(a, b);
+    *reinterpret_cast<VT*>(y) = a;
+    if (HALVES) *reinterpret_cast<VT*>(y + pairs) = b;
   }
 }
 
@@ -132,8 +189,7 @@ cudaError_t launch_v(const RopeTurns& t, RopeArgs a, int tokens, int head_dim, c
   const long long blocks = (a.work + ROPE_THREADS - 1) / ROPE_THREADS;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)((a.heads + hpt - 1) / hpt));
-  rope_kernel<T, V, HALVES, ALIGN><<<grid, ROPE_THREADS, 0, st>>>(t, a);
-  return cudaGetLastError();
+  return launch_op(rope_kernel<T, V, HALVES, ALIGN>, grid, ROPE_THREADS, 0, 1, st, t, a);
 }
 
 // The widest vector (up to 16 bytes) that every address is a multiple of.
