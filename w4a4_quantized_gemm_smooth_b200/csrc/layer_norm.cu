@@ -13,8 +13,7 @@
 //
 // Backward: a thread owns fixed columns; their sums of dy xhat and dy stay in
 // its registers over all the rows of the team and are joined at the end:
-// teams of a block in shared memory in order, blocks of a group through fp32
-// partials in the workspace, summed in block order by a second kernel.  X and
+// teams of a block in shared memory, blocks of a group through fp32 partials in the workspace, summed in block order by a second kernel.  X and
 // dY are read once.
 #include <climits>
 #include <cmath>
@@ -75,7 +74,7 @@ struct NormCfg {
   static constexpr size_t FWD_SMEM = RING_FWD + 2 * PARAM;
   static constexpr size_t BWD_SMEM = RING_BWD + PARAM;
   static_assert(FWD_SMEM <= 227 * 1024 && BWD_SMEM <= 227 * 1024, "shared memory");
-  static_assert(TEAMS == 1 || (size_t)2 * NV * G * V * 4 <= RING_BWD, "column sums fit the ring");
+  static_assert(TEAMS == 1 || (size_t)2 * NV * THREADS * V * 4 <= RING_BWD, "the teams' sums fit the ring");
 };
 
 // A thread's share of a row: vectors at elements c(i) = (lane + i G) V, and
@@ -152,20 +151,38 @@ __device__ __forceinline__ void read_param(float2 (&out)[V / 2], const float4* s
 }
 
 // Sums over a team of G threads (G = 32: the warp; else the whole block) of
-// R values.  `red` has room for R G / 32 values; successive calls alternate
-// between two of them, so that one barrier per call is enough.
+// R values (1, 2 or 4) that every thread then has.  Inside a warp the values
+// are scattered over the lanes while they are summed, which takes 4 to 6
+// exchanges instead of 5 R.  `red` has room for R G / 32 values; successive
+// calls alternate between two of them, so that one barrier per call is enough.
 template <int G, int R>
 __device__ __forceinline__ void team_sum(float (&v)[R], float* red) {
+  const int lane = threadIdx.x & 31;
+  float c;
+  if constexpr (R == 4) {
+    const bool h = lane & 16;
+    float a = h ? v[2] : v[0], b = h ? v[3] : v[1];
+    a += __shfl_xor_sync(0xFFFFFFFFu, h ? v[0] : v[2], 16);
+    b += __shfl_xor_sync(0xFFFFFFFFu, h ? v[1] : v[3], 16);
+    const bool g = lane & 8;
+    c = (g ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, g ? a : b, 8);
+  } else if constexpr (R == 2) {
+    const bool h = lane & 16;
+    c = (h ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, h ? v[0] : v[1], 16);
+    c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
+  } else {
+    c = v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
+    c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+  constexpr int L = 32 / R;                  // lanes that hold one value
+  if constexpr (G == 32) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-  if constexpr (G > 32) {
+    for (int k = 0; k < R; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, c, k * L);
+  } else {
     constexpr int W = G / 32;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int k = 0; k < R; ++k) red[k * W + (threadIdx.x >> 5)] = v[k];
-    }
+    if (lane % L == 0) red[(lane / L) * W + (threadIdx.x >> 5)] = c;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -480,60 +497,69 @@ norm_bwd_kernel(const NormBwdArgs p) {
     slot = slot + 1 == D ? 0 : slot + 1;
   }
   if constexpr (PARAMS) {
-    if constexpr (TEAMS > 1) {
-      // join the teams in order, where the rows were (none is in flight)
-      constexpr int COLS = NV * G * V;
-      float2* cw = reinterpret_cast<float2*>(smem);
-      float2* cb = cw + COLS / 2;
-      cp_async_wait<0>();
-      __syncthreads();
-      for (int k = 0; k < TEAMS; ++k) {
-        if (team == k) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < H; ++j) {
-              const int c = (lane + i * G) * H + j;
-              if (k > 0) {
-                aw[i][j] = __fadd2_rn(cw[c], aw[i][j]);
-                ab[i][j] = __fadd2_rn(cb[c], ab[i][j]);
-              }
-              if (k < TEAMS - 1) {
-                cw[c] = aw[i][j];
-                cb[c] = ab[i][j];
-              }
-            }
-        }
-        __syncthreads();
-      }
-      if (team != TEAMS - 1) return;
-    }
     const bool whole = p.splits == 1;
-    // an own row of the gradients, or this block's partial row
+    // an own row of the gradients, or this block's partial row (of whole vectors)
     PT* dw = whole && p.dw ? static_cast<PT*>(p.dw) + span.g * p.lddw : nullptr;
     PT* db = whole && p.db ? static_cast<PT*>(p.db) + span.g * p.lddb : nullptr;
-    // partial rows of K rounded up to 8 elements: whole vectors
     float* part = p.part + (whole ? 0 : (size_t)blockIdx.x * 2 * part_pitch(p.K));
+    if constexpr (TEAMS == 1) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (lane + i * G) * V;
-      if (c >= p.K) continue;
-      if (whole) {
-        RowVec<PT, V> ow, ob;
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * G) * V;
+        if (c >= p.K) continue;
+        if (whole) {
+          RowVec<PT, V> ow, ob;
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-          ow.set(j, aw[i][j]);
-          ob.set(j, ab[i][j]);
+          for (int j = 0; j < H; ++j) {
+            ow.set(j, aw[i][j]);
+            ob.set(j, ab[i][j]);
+          }
+          if (dw) store_vec<PT, V>(dw, c, p.K, ow);
+          if (db) store_vec<PT, V>(db, c, p.K, ob);
+        } else {
+          float4* dst_w = reinterpret_cast<float4*>(part + c);
+          float4* dst_b = reinterpret_cast<float4*>(part + part_pitch(p.K) + c);
+#pragma unroll
+          for (int j = 0; j < H; j += 2) {
+            dst_w[j / 2] = make_float4(aw[i][j].x, aw[i][j].y, aw[i][j + 1].x, aw[i][j + 1].y);
+            dst_b[j / 2] = make_float4(ab[i][j].x, ab[i][j].y, ab[i][j + 1].x, ab[i][j + 1].y);
+          }
         }
-        if (dw) store_vec<PT, V>(dw, c, p.K, ow);
-        if (db) store_vec<PT, V>(db, c, p.K, ob);
-      } else {
-        float4* dst_w = reinterpret_cast<float4*>(part + c);
-        float4* dst_b = reinterpret_cast<float4*>(part + part_pitch(p.K) + c);
+      }
+    } else {
+      // the teams' sums meet where the rows were (none is in flight), and
+      // every thread adds up some columns over the teams, in order
+      constexpr int COLS = NV * G * V;
+      float* meet = reinterpret_cast<float*>(smem);       // [team][2][COLS]
+      cp_async_wait<0>();
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < H; j += 2) {
-          dst_w[j / 2] = make_float4(aw[i][j].x, aw[i][j].y, aw[i][j + 1].x, aw[i][j + 1].y);
-          dst_b[j / 2] = make_float4(ab[i][j].x, ab[i][j].y, ab[i][j + 1].x, ab[i][j + 1].y);
+          const int c = (lane + i * G) * V + 2 * j;
+          float* at = meet + team * 2 * COLS + c;
+          *reinterpret_cast<float4*>(at) = make_float4(aw[i][j].x, aw[i][j].y, aw[i][j + 1].x, aw[i][j + 1].y);
+          *reinterpret_cast<float4*>(at + COLS) = make_float4(ab[i][j].x, ab[i][j].y, ab[i][j + 1].x, ab[i][j + 1].y);
+        }
+      __syncthreads();
+      for (int u = threadIdx.x; u < 2 * COLS / 4; u += TH) {
+        const int which = u >= COLS / 4, c = 4 * u - which * COLS;
+        if (c >= p.K) continue;
+        float4 s = *reinterpret_cast<const float4*>(meet + 4 * u);
+#pragma unroll
+        for (int t = 1; t < TEAMS; ++t) {
+          const float4 v = *reinterpret_cast<const float4*>(meet + t * 2 * COLS + 4 * u);
+          s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        if (whole) {
+          PT* out = which ? db : dw;
+          const float e[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (out && c + k < p.K) out[c + k] = Elem<PT>::from_f(e[k]);
+        } else {
+          *reinterpret_cast<float4*>(part + (which ? part_pitch(p.K) : 0) + c) = s;
         }
       }
     }
@@ -541,33 +567,41 @@ norm_bwd_kernel(const NormBwdArgs p) {
 }
 
 // Sums the blocks' partials of every group and column in block order: 32
-// columns by 8 rows of threads, each row summing a contiguous eighth of the
-// blocks, then the eighths in order.
+// columns (a float4 a thread) by 32 threads that each take a contiguous share
+// of the blocks, then the shares in order.
 template <typename PT>
 __global__ void __launch_bounds__(256)
 norm_bwd_join_kernel(const float* part, int splits, int K, PT* dw, long long lddw, PT* db,
                      long long lddb) {
-  __shared__ float sh[8][33];
-  grid_wait();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + tx;
+  __shared__ float4 sh[32][8];
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+  const int c = blockIdx.x * 32 + tx * 4;
   const int which = blockIdx.y & 1;
   const long long g = blockIdx.z;
-  float acc = 0.0f;
+  grid_wait();
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const size_t pitch = part_pitch(K);
   if (c < K) {
-    const int s0 = splits * ty / 8, s1 = splits * (ty + 1) / 8;
-    const size_t pitch = part_pitch(K);
+    const int s0 = splits * ty / 32, s1 = splits * (ty + 1) / 32;
     const float* q = part + (((size_t)g * splits + s0) * 2 + which) * pitch + c;
 #pragma unroll 8
-    for (int s = s0; s < s1; ++s, q += 2 * pitch) acc += *q;
+    for (int s = s0; s < s1; ++s, q += 2 * pitch) {
+      const float4 v = *reinterpret_cast<const float4*>(q);
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
   }
   sh[ty][tx] = acc;
   __syncthreads();
-  if (ty == 0 && c < K) {
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && col < K) {
+    float s = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += sh[i][tx];
+    for (int i = 0; i < 32; ++i) s += reinterpret_cast<const float*>(sh[i])[threadIdx.x];
     PT* out = which ? db : dw;
-    if (out) out[g * (which ? lddb : lddw) + c] = Elem<PT>::from_f(acc);
+    if (out) out[g * (which ? lddb : lddw) + col] = Elem<PT>::from_f(s);
   }
 }
 

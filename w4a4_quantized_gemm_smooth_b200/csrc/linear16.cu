@@ -54,15 +54,23 @@ dp_kernel(const DpArgs a) {
   const long long r0 = (long long)blockIdx.y * a.rows_per_block;
   const long long r1 = min((long long)a.M, r0 + a.rows_per_block);
   float2 acc[4] = {};
-  if (c < a.N) {
-    // DP_ROWS rows at a time, so that their loads are in flight together
+  auto walk = [&](auto whole) {
+    // whole: the thread's eight columns lie in the row (vector accesses).
+    // DP_ROWS rows at a time, so that their loads are in flight together.
+    constexpr bool WHOLE = decltype(whole)::value;
+    const uint16_t* dy = a.dy + c;
+    const uint16_t* pp = a.p + c;
+    uint16_t* dp = a.dp + c;
+    const int n = WHOLE ? 8 : a.N - c;
     for (long long r = r0 + ty; r < r1; r += 8 * DP_ROWS) {
       uint4 d4[DP_ROWS], p4[DP_ROWS];
 #pragma unroll
       for (int k = 0; k < DP_ROWS; ++k) {
-        const bool in = r + 8 * k < r1;
-        d4[k] = in ? load8(a.dy + (r + 8 * k) * a.lddy, c, a.N) : make_uint4(0, 0, 0, 0);
-        p4[k] = in && a.p ? load8(a.p + (r + 8 * k) * a.ldp, c, a.N) : make_uint4(0, 0, 0, 0);
+        d4[k] = p4[k] = make_uint4(0, 0, 0, 0);
+        if (r + 8 * k < r1) {
+          d4[k] = load8(dy + (r + 8 * k) * a.lddy, 0, n);
+          if (EPI != SVDQ_EPI_NONE) p4[k] = load8(pp + (r + 8 * k) * a.ldp, 0, n);
+        }
       }
 #pragma unroll
       for (int k = 0; k < DP_ROWS; ++k) {
@@ -76,10 +84,14 @@ dp_kernel(const DpArgs a) {
           dw[e] = pack2(d, bf16);
         }
         if (EPI != SVDQ_EPI_NONE && r + 8 * k < r1)
-          store8(a.dp + (r + 8 * k) * a.lddp, c, a.N, make_uint4(dw[0], dw[1], dw[2], dw[3]));
+          store8(dp + (r + 8 * k) * a.lddp, 0, n, make_uint4(dw[0], dw[1], dw[2], dw[3]));
       }
     }
-  }
+  };
+  if (c + 8 <= a.N)
+    walk(std::true_type());
+  else if (c < a.N)
+    walk(std::false_type());
   if (!a.part) return;
   __shared__ float sh[8][DP_COLS + 8];
 #pragma unroll
@@ -97,24 +109,25 @@ dp_kernel(const DpArgs a) {
   }
 }
 
-// db = the row blocks' sums in order: 32 columns by 8 rows of threads.
-__global__ void __launch_bounds__(256)
+// db = the row blocks' sums in order: 32 columns by 32 rows of threads, each
+// summing a contiguous share of the blocks, then the shares in order.
+__global__ void __launch_bounds__(1024)
 db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
-  __shared__ float sh[8][33];
+  __shared__ float sh[32][33];
   grid_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   float acc = 0.0f;
   if (c < N) {
-    const int b0 = blocks * ty / 8, b1 = blocks * (ty + 1) / 8;
-#pragma unroll 8
+    const int b0 = blocks * ty / 32, b1 = blocks * (ty + 1) / 32;
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) acc += part[(size_t)b * N + c];
   }
   sh[ty][tx] = acc;
   __syncthreads();
   if (ty == 0 && c < N) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += sh[i][tx];
+    for (int i = 1; i < 32; ++i) acc += sh[i][tx];
     db[c] = (uint16_t)pack2(make_float2(acc, 0.0f), bf16 != 0);
   }
 }
@@ -322,7 +335,7 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
                   : epilogue == SVDQ_EPI_SILU ? svdq::dp_kernel<SVDQ_EPI_SILU>
                                               : svdq::dp_kernel<SVDQ_EPI_NONE>;
     if (svdq::launch_op(kernel, grid, 256, 0, 1, stream, d) != cudaSuccess) return SVDQ_ERR_CUDA;
-    if (db && svdq::launch_op(svdq::db_join_kernel, dim3((unsigned)(((long long)N + 31) / 32)), 256, 0,
+    if (db && svdq::launch_op(svdq::db_join_kernel, dim3((unsigned)(((long long)N + 31) / 32)), 1024, 0,
                               1, stream, d.part, blocks, N, static_cast<uint16_t*>(db),
                               bf16) != cudaSuccess)
       return SVDQ_ERR_CUDA;
