@@ -447,6 +447,30 @@ def test_norm_backward_without_weight():
     check_norm_bwd(300, 1152, BF16, BF16, affine=False)
 
 
+@pytest.mark.parametrize("scale", [1e-18, 1e15])
+@pytest.mark.parametrize("K", [96, 1300])
+def test_norm_of_very_small_and_large_rows(scale, K):
+    """eps = 0 and rows whose spread is far from 1 (its square is in fp32's
+    range): nothing else on the way leaves that range."""
+    g = gen(31)
+    X, dY = rows(g, 20, K, F32), rows(g, 20, K, F32)
+    X *= scale
+    x = X.double()
+    mu = x.mean(1, keepdim=True)
+    rstd = ((x - mu) ** 2).mean(1, keepdim=True).rsqrt()
+    Y, mean, rs = out(20, K, F32), torch.empty(20, device="cuda"), torch.empty(20, device="cuda")
+    S.svdq_layer_norm(X, Y, eps=0.0, mean=mean, rstd=rs)
+    ref = (x - mu) * rstd
+    assert float((Y.double() - ref).abs().max()) <= 2.0 ** -15        # 80 roundings of values up to 5
+    dX, dw = out(20, K, F32), torch.empty((K,), device="cuda")
+    ws = torch.empty((max(S.svdq_layer_norm_backward_workspace(20, K), 1),), dtype=torch.uint8, device="cuda")
+    S.svdq_layer_norm_backward(dY, X, mean, rs, dX, dweight=dw, workspace=ws)
+    t, h = dY.double(), (x - mean.double()[:, None]) * rs.double()[:, None]
+    refd = rs.double()[:, None] * (t - t.mean(1, keepdim=True) - h * (t * h).mean(1, keepdim=True))
+    assert bool(((dX.double() - refd).abs() <= 2.0 ** -15 * rs.double()[:, None]).all())
+    assert bool(((dw.double() - (t * h).sum(0)).abs() <= 2.0 ** -18 * (t * h).abs().sum(0)).all())
+
+
 def test_norm_gradients_against_differences():
     g = gen(4)
     M, K, rpg = 12, 96, 5

@@ -1,10 +1,11 @@
 // Layer norm with a scale and a shift per group of rows, and its gradients.
 //
 // A row belongs to one team (a warp, or a block of 128 or 512 threads for
-// long rows), and a team walks over rows of one group.  Each thread copies
-// its own 16-byte vectors of the next rows to its own places in shared
-// memory (cp.async, no barrier), so that the bytes in flight do not depend
-// on the registers that a row needs; the scale and the shift wait there too.
+// long rows), and a team walks over rows of one group, two at a time.  Each
+// thread copies its own 16-byte vectors of the next rows to its own places in
+// shared memory (cp.async, no barrier), so that the bytes in flight do not
+// depend on the registers that a row needs; the group's scale (with its
+// offset) and shift wait there too, in fp32, converted once per block.
 // Arithmetic runs on pairs (packed fp32 instructions), which keeps it below
 // the memory time.
 //
@@ -13,8 +14,9 @@
 //
 // Backward: a thread owns fixed columns; their sums of dy xhat and dy stay in
 // its registers over all the rows of the team and are joined at the end:
-// teams of a block in shared memory, blocks of a group through fp32 partials in the workspace, summed in block order by a second kernel.  X and
-// dY are read once.
+// teams of a block in shared memory, blocks of a group through fp32 partials
+// in the workspace, summed in block order by a second kernel.  X and dY are
+// read once.
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -440,15 +442,14 @@ norm_bwd_kernel(const NormBwdArgs p) {
         const RowVec<T, V> dr = read_vec<T, V>(q + ((2 * k + 1) * NV + i) * TH, TH);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-          const float2 d = dr.get(j);
-          const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m[k]), r[k]);
+          const float2 g = dr.get(j), d = __fadd2_rn(xr.get(j), m[k]);     // xhat = d r
           if constexpr (PARAMS) {
-            aw[i][j] = __ffma2_rn(d, h, aw[i][j]);
-            ab[i][j] = __fadd2_rn(ab[i][j], d);
+            aw[i][j] = __ffma2_rn(__fmul2_rn(g, r[k]), d, aw[i][j]);
+            ab[i][j] = __fadd2_rn(ab[i][j], g);
           }
-          const float2 t = w ? __fmul2_rn(d, f[j]) : d;
+          const float2 t = w ? __fmul2_rn(g, f[j]) : g;
           s1[k] = __fadd2_rn(s1[k], t);
-          s2[k] = __ffma2_rn(t, h, s2[k]);
+          s2[k] = __ffma2_rn(t, d, s2[k]);
         }
       }
     }
@@ -465,8 +466,10 @@ norm_bwd_kernel(const NormBwdArgs p) {
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        s1[k] = splat2(-sum[2 * k] * inv_k);
-        s2[k] = splat2(-sum[2 * k + 1] * inv_k);
+        // dX = r t - r mean(t) - xhat r mean(t xhat)
+        const float rs = r[k].x;
+        s1[k] = splat2(-sum[2 * k] * inv_k * rs);
+        s2[k] = splat2(-sum[2 * k + 1] * rs * inv_k * rs);
       }
       T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
@@ -482,10 +485,9 @@ norm_bwd_kernel(const NormBwdArgs p) {
             RowVec<T, V> o;
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-              const float2 d = dr.get(j);
-              const float2 h = __fmul2_rn(__fadd2_rn(xr.get(j), m[k]), r[k]);
-              const float2 t = w ? __fmul2_rn(d, f[j]) : d;
-              o.set(j, __fmul2_rn(r[k], __ffma2_rn(h, s2[k], __fadd2_rn(t, s1[k]))));
+              const float2 g = dr.get(j), d = __fadd2_rn(xr.get(j), m[k]);
+              const float2 t = w ? __fmul2_rn(g, f[j]) : g;
+              o.set(j, __ffma2_rn(t, r[k], __ffma2_rn(__fmul2_rn(d, r[k]), s2[k], s1[k])));
             }
             if (k == 0 || row + k < span.r1)
               store_vec<T, V>(dx + k * p.lddx, c, i + 1 < NV ? INT_MAX : p.K, o);
