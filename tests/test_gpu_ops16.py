@@ -117,6 +117,13 @@ def test_linear_sizes(M, K, N, dtype):
     check_linear(M, K, N, dtype, S.EPI_GELU, seed=M + K + N)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("K,N", [(1, 1), (8, 4736), (250, 4737), (4096, 33), (4097, 5000), (8200, 50), (12287, 129)])
+def test_linear_few_rows(M, K, N):
+    for dtype in (BF16, F16):
+        check_linear(M, K, N, dtype, S.EPI_SILU, seed=M + K)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("epi", [S.EPI_NONE, S.EPI_GELU, S.EPI_SILU])
 @pytest.mark.parametrize("bias,res,pre", [(False, False, False), (True, False, False), (False, True, False),
