@@ -490,14 +490,19 @@ def svdq_debug_partials(w: Weights, M, xq, row0, nrows, col0, ncols, P, stream=N
 
 _torch = None
 _DTYPES: dict = {}
+_F32 = None
+
+
+def _load_torch():
+    global _torch, _F32
+    import torch
+    _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _torch, _F32 = torch, torch.float32
 
 
 def _dtype_code(t, name="X"):
-    global _torch
     if _torch is None:
-        import torch
-        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-        _torch = torch
+        _load_torch()
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: dtype {t.dtype} is not supported")
@@ -509,35 +514,29 @@ def _raw_stream(stream, dev):
     tensors' one), which has to be the current device: launches go there."""
     if dev < 0:
         raise ValueError("the tensors have to be on a CUDA device")
-    if dev != _torch.cuda.current_device():
+    if dev != _torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
     if stream is None:
         return _torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
 
 
-def _matrix(t, name, rows, cols, dtype, dev):
-    """(pointer, leading dimension) of a [rows, cols] tensor of type `dtype`
-    on device `dev` with contiguous rows."""
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+def _matrix(t, name, shape, dtype, dev):
+    """(pointer, leading dimension) of a tensor of this shape (two sizes) and
+    type on device `dev`, with contiguous rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype or t.get_device() != dev:
         raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype} on cuda:{dev}")
     ld, one = t.stride()
-    if one != 1 and cols > 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: rows have to be contiguous")
-    if rows <= 1:
-        ld = -(-cols // 8) * 8          # a single row has no pitch
+    if shape[0] <= 1:
+        ld = -(-shape[1] // 8) * 8          # a single row has no pitch
     return t.data_ptr(), ld
 
 
-def _opt_matrix(t, name, rows, cols, dtype, dev):
-    return (None, 0) if t is None else _matrix(t, name, rows, cols, dtype, dev)
-
-
-def _opt_vector(t, name, n, dtype, dev):
-    if t is None:
-        return None
+def _vector(t, name, n, dtype, dev):
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name}: expected {n} contiguous values")
     if t.dtype != dtype or t.get_device() != dev:
@@ -557,18 +556,24 @@ def svdq_linear16(X, W, Y, bias=None, residual=None, epilogue=EPI_NONE, preact=N
     """Y = epi(X W^T + bias) + residual.  X [M, K], W [N, K], Y [M, N], all
     cuda bf16 or fp16 with contiguous rows; bias [N]; residual [M, N] (may be
     Y); preact [M, N] receives X W^T + bias for svdq_linear16_backward."""
-    code, dev, dt = _dtype_code(X), X.get_device(), X.dtype
-    M, K = X.shape
+    code, dev, dt, xshape = _dtype_code(X), X.get_device(), X.dtype, X.shape
+    M, K = xshape
     N = W.shape[0]
     st = _raw_stream(stream, dev)
-    x, ldx = _matrix(X, "X", M, K, dt, dev)
-    w, ldw = _matrix(W, "W", N, K, dt, dev)
-    y, ldy = _matrix(Y, "Y", M, N, dt, dev)
-    b = _opt_vector(bias, "bias", N, dt, dev)
-    r, ldr = _opt_matrix(residual, "residual", M, N, dt, dev)
-    p, ldp = _opt_matrix(preact, "preact", M, N, dt, dev)
-    _check(lib().svdq_linear16(code, M, K, N, x, ldx, w, ldw, b, r, ldr, epilogue, y, ldy, p, ldp,
-                               st), "svdq_linear16")
+    x, ldx = _matrix(X, "X", xshape, dt, dev)
+    w, ldw = _matrix(W, "W", (N, K), dt, dev)
+    y, ldy = _matrix(Y, "Y", (M, N), dt, dev)
+    b = r = p = None
+    ldr = ldp = 0
+    if bias is not None:
+        b = _vector(bias, "bias", N, dt, dev)
+    if residual is not None:
+        r, ldr = _matrix(residual, "residual", (M, N), dt, dev)
+    if preact is not None:
+        p, ldp = _matrix(preact, "preact", (M, N), dt, dev)
+    rc = lib().svdq_linear16(code, M, K, N, x, ldx, w, ldw, b, r, ldr, epilogue, y, ldy, p, ldp, st)
+    if rc:
+        raise SVDQError(rc, "svdq_linear16")
 
 
 def svdq_linear16_backward_workspace(M: int, K: int, N: int, epilogue=EPI_NONE) -> int:
@@ -588,13 +593,21 @@ def svdq_linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue=
     else:
         K = (X if X is not None else W).shape[1]
     st = _raw_stream(stream, dev)
-    d, ldd = _matrix(dY, "dY", M, N, dt, dev)
-    x, ldx = _opt_matrix(X, "X", M, K, dt, dev)
-    w, ldw = _opt_matrix(W, "W", N, K, dt, dev)
-    p, ldp = _opt_matrix(preact, "preact", M, N, dt, dev)
-    gx, ldgx = _opt_matrix(dX, "dX", M, K, dt, dev)
-    gw, ldgw = _opt_matrix(dW, "dW", N, K, dt, dev)
-    gb = _opt_vector(dbias, "dbias", N, dt, dev)
+    d, ldd = _matrix(dY, "dY", (M, N), dt, dev)
+    x = w = p = gx = gw = gb = None
+    ldx = ldw = ldp = ldgx = ldgw = 0
+    if X is not None:
+        x, ldx = _matrix(X, "X", (M, K), dt, dev)
+    if W is not None:
+        w, ldw = _matrix(W, "W", (N, K), dt, dev)
+    if preact is not None:
+        p, ldp = _matrix(preact, "preact", (M, N), dt, dev)
+    if dX is not None:
+        gx, ldgx = _matrix(dX, "dX", (M, K), dt, dev)
+    if dW is not None:
+        gw, ldgw = _matrix(dW, "dW", (N, K), dt, dev)
+    if dbias is not None:
+        gb = _vector(dbias, "dbias", N, dt, dev)
     ws, nbytes = _opt_workspace(workspace, dev)
     _check(lib().svdq_linear16_backward(code, M, K, N, d, ldd, x, ldx, w, ldw, p, ldp, epilogue,
                                         gx, ldgx, gw, ldgw, gb, ws, nbytes, st),
@@ -607,36 +620,32 @@ def svdq_get_op_error(stream=None):
     _check(lib().svdq_get_op_error(_stream_ptr(stream)), "device")
 
 
-def _params(t, name, groups, K, dev, shared=True):
+def _params(t, name, groups, K, dtype, dev, shared=True):
     """(pointer, leading dimension) of a parameter [groups, K] or [K] (shared
     by every group); a gradient (not shared) has a row per group."""
-    if t is None:
-        return None, 0
     shape = t.shape
-    if t.get_device() != dev or len(shape) not in (1, 2) or shape[-1] != K or \
-            (K > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name}: expected [{groups}, {K}] or [{K}] with contiguous rows on cuda:{dev}")
-    if len(shape) == 1 or shape[0] == 1:
+    if shape == (K,) or shape == (1, K):
         if not shared and groups != 1:
             raise ValueError(f"{name}: expected [{groups}, {K}]")
-        return t.data_ptr(), 0 if shared else -(-K // 8) * 8
-    if shape[0] != groups:
-        raise ValueError(f"{name}: expected {groups} rows")
-    return t.data_ptr(), t.stride(0)
+        ld = 0 if shared else -(-K // 8) * 8
+    elif shape == (groups, K):
+        ld = t.stride(0)
+    else:
+        raise ValueError(f"{name}: expected [{groups}, {K}] or [{K}]")
+    if t.get_device() != dev or t.dtype != dtype or (t.stride()[-1] != 1 and K > 1):
+        raise ValueError(f"{name}: expected contiguous rows of {dtype} on cuda:{dev}")
+    return t.data_ptr(), ld
 
 
-def _param_code(X, *ps):
-    """The parameters' common type code (X's type or float32)."""
-    dt = None
+def _param_dtype(X, *ps):
+    """The parameters' common type (X's type or float32) and its code."""
     for p in ps:
         if p is not None:
-            if dt is not None and p.dtype != dt:
-                raise ValueError("the parameters and their gradients have to be of one type")
-            dt = p.dtype
-    code = _DTYPES.get(X.dtype if dt is None else dt)
-    if code is None:
-        raise ValueError(f"parameters: dtype {dt} is not supported")
-    return code
+            code = _DTYPES.get(p.dtype)
+            if code is None:
+                raise ValueError(f"parameters: dtype {p.dtype} is not supported")
+            return p.dtype, code
+    return X.dtype, _DTYPES[X.dtype]
 
 
 def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, rows_per_group=0,
@@ -645,19 +654,27 @@ def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, r
     [M, K] (bf16, fp16 or fp32).  weight, bias: [K], or [groups, K] with one
     row for every rows_per_group rows of X; X's type or fp32.  mean, rstd:
     fp32 [M], the statistics for svdq_layer_norm_backward.  Y may be X."""
-    code, dev, dt = _dtype_code(X), X.get_device(), X.dtype
-    M, K = X.shape
+    code, dev, dt, shape = _dtype_code(X), X.get_device(), X.dtype, X.shape
+    M, K = shape
     st = _raw_stream(stream, dev)
-    x, ldx = _matrix(X, "X", M, K, dt, dev)
-    y, ldy = _matrix(Y, "Y", M, K, dt, dev)
-    pc = _param_code(X, weight, bias)
+    x, ldx = _matrix(X, "X", shape, dt, dev)
+    y, ldy = _matrix(Y, "Y", shape, dt, dev)
+    pdt, pc = _param_dtype(X, weight, bias)
     groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
-    w, ldw = _params(weight, "weight", groups, K, dev)
-    b, ldb = _params(bias, "bias", groups, K, dev)
-    mu = _opt_vector(mean, "mean", M, _torch.float32, dev)
-    rs = _opt_vector(rstd, "rstd", M, _torch.float32, dev)
-    _check(lib().svdq_layer_norm(code, pc, M, K, x, ldx, w, ldw, b, ldb, weight_offset,
-                                 rows_per_group, eps, y, ldy, mu, rs, st), "svdq_layer_norm")
+    w = b = mu = rs = None
+    ldw = ldb = 0
+    if weight is not None:
+        w, ldw = _params(weight, "weight", groups, K, pdt, dev)
+    if bias is not None:
+        b, ldb = _params(bias, "bias", groups, K, pdt, dev)
+    if mean is not None:
+        mu = _vector(mean, "mean", M, _F32, dev)
+    if rstd is not None:
+        rs = _vector(rstd, "rstd", M, _F32, dev)
+    rc = lib().svdq_layer_norm(code, pc, M, K, x, ldx, w, ldw, b, ldb, weight_offset,
+                               rows_per_group, eps, y, ldy, mu, rs, st)
+    if rc:
+        raise SVDQError(rc, "svdq_layer_norm")
 
 
 def svdq_layer_norm_backward_workspace(M: int, K: int, rows_per_group: int = 0) -> int:
@@ -670,19 +687,25 @@ def svdq_layer_norm_backward(dY, X, mean, rstd, dX, weight=None, weight_offset=0
                              stream=None):
     """Gradients of svdq_layer_norm: dX [M, K] (may be dY or X), dweight and
     dbias [groups, K] or, with one group, [K]; each may be None."""
-    code, dev, dt = _dtype_code(X), X.get_device(), X.dtype
-    M, K = X.shape
+    code, dev, dt, shape = _dtype_code(X), X.get_device(), X.dtype, X.shape
+    M, K = shape
     st = _raw_stream(stream, dev)
-    d, ldd = _matrix(dY, "dY", M, K, dt, dev)
-    x, ldx = _matrix(X, "X", M, K, dt, dev)
-    gx, ldgx = _opt_matrix(dX, "dX", M, K, dt, dev)
-    pc = _param_code(X, weight, dweight, dbias)
+    d, ldd = _matrix(dY, "dY", shape, dt, dev)
+    x, ldx = _matrix(X, "X", shape, dt, dev)
+    pdt, pc = _param_dtype(X, weight, dweight, dbias)
     groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
-    w, ldw = _params(weight, "weight", groups, K, dev)
-    gw, ldgw = _params(dweight, "dweight", groups, K, dev, False)
-    gb, ldgb = _params(dbias, "dbias", groups, K, dev, False)
-    mu = _opt_vector(mean, "mean", M, _torch.float32, dev)
-    rs = _opt_vector(rstd, "rstd", M, _torch.float32, dev)
+    gx = w = gw = gb = None
+    ldgx = ldw = ldgw = ldgb = 0
+    if dX is not None:
+        gx, ldgx = _matrix(dX, "dX", shape, dt, dev)
+    if weight is not None:
+        w, ldw = _params(weight, "weight", groups, K, pdt, dev)
+    if dweight is not None:
+        gw, ldgw = _params(dweight, "dweight", groups, K, pdt, dev, False)
+    if dbias is not None:
+        gb, ldgb = _params(dbias, "dbias", groups, K, pdt, dev, False)
+    mu = _vector(mean, "mean", M, _F32, dev)
+    rs = _vector(rstd, "rstd", M, _F32, dev)
     ws, nbytes = _opt_workspace(workspace, dev)
     _check(lib().svdq_layer_norm_backward(code, pc, M, K, d, ldd, x, ldx, mu, rs, w, ldw,
                                           weight_offset, rows_per_group, gx, ldgx, gw, ldgw, gb,
@@ -750,8 +773,10 @@ def svdq_rope(plan: RopePlan, positions, X, out, inverse=False, stream=None):
     R = pshape[0]
     ldp = positions.stride(0) if R > 1 else axes
     st = _raw_stream(stream, dev)
-    _check(lib().svdq_rope(plan._h, code, T, H, D, positions.data_ptr(), R, ldp, X.data_ptr(), xt,
-                           xh, out.data_ptr(), yt, yh, 1 if inverse else 0, st), "svdq_rope")
+    rc = lib().svdq_rope(plan._h, code, T, H, D, positions.data_ptr(), R, ldp, X.data_ptr(), xt, xh,
+                         out.data_ptr(), yt, yh, 1 if inverse else 0, st)
+    if rc:
+        raise SVDQError(rc, "svdq_rope")
 
 
 class SVDQLinear:
