@@ -486,7 +486,9 @@ def svdq_debug_partials(w: Weights, M, xq, row0, nrows, col0, ncols, P, stream=N
 # tensors, so the binding checks each one's device, type and shape before it
 # passes the pointer on (ValueError); the library checks sizes and alignment.
 
-# They are written for a short host path: a call costs a few microseconds.
+# The three calls that one token makes (svdq_linear16, svdq_layer_norm and
+# svdq_rope) make the same checks in a small CPython module, since a call
+# through ctypes takes the host longer than the device.
 
 _torch = None
 _DTYPES: dict = {}
@@ -498,6 +500,31 @@ def _load_torch():
     import torch
     _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     _torch, _F32 = torch, torch.float32
+
+
+_fast = None
+
+
+def _fastcall():
+    """The CPython binding (_lib/_svdq_fastcall.so, built with the library).
+    Raises if it is missing."""
+    global _fast
+    if _fast is None:
+        import importlib.util
+        lib()
+        path = os.path.join(_PKG, "_lib", "_svdq_fastcall.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it with "
+                "`python -m w4a4_quantized_gemm_smooth_b200.build` (no fallback exists)")
+        spec = importlib.util.spec_from_file_location("_svdq_fastcall", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        import torch
+        mod.init((torch.bfloat16, torch.float16, torch.float32), torch.int32,
+                 torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _fast = mod
+    return _fast
 
 
 def _dtype_code(t, name="X"):
@@ -556,22 +583,8 @@ def svdq_linear16(X, W, Y, bias=None, residual=None, epilogue=EPI_NONE, preact=N
     """Y = epi(X W^T + bias) + residual.  X [M, K], W [N, K], Y [M, N], all
     cuda bf16 or fp16 with contiguous rows; bias [N]; residual [M, N] (may be
     Y); preact [M, N] receives X W^T + bias for svdq_linear16_backward."""
-    code, dev, dt, xshape = _dtype_code(X), X.get_device(), X.dtype, X.shape
-    M, K = xshape
-    N = W.shape[0]
-    st = _raw_stream(stream, dev)
-    x, ldx = _matrix(X, "X", xshape, dt, dev)
-    w, ldw = _matrix(W, "W", (N, K), dt, dev)
-    y, ldy = _matrix(Y, "Y", (M, N), dt, dev)
-    b = r = p = None
-    ldr = ldp = 0
-    if bias is not None:
-        b = _vector(bias, "bias", N, dt, dev)
-    if residual is not None:
-        r, ldr = _matrix(residual, "residual", (M, N), dt, dev)
-    if preact is not None:
-        p, ldp = _matrix(preact, "preact", (M, N), dt, dev)
-    rc = lib().svdq_linear16(code, M, K, N, x, ldx, w, ldw, b, r, ldr, epilogue, y, ldy, p, ldp, st)
+    rc = (_fast or _fastcall()).linear16(X, W, Y, bias, residual, epilogue, preact,
+                                         None if stream is None else stream.cuda_stream)
     if rc:
         raise SVDQError(rc, "svdq_linear16")
 
@@ -654,25 +667,9 @@ def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, r
     [M, K] (bf16, fp16 or fp32).  weight, bias: [K], or [groups, K] with one
     row for every rows_per_group rows of X; X's type or fp32.  mean, rstd:
     fp32 [M], the statistics for svdq_layer_norm_backward.  Y may be X."""
-    code, dev, dt, shape = _dtype_code(X), X.get_device(), X.dtype, X.shape
-    M, K = shape
-    st = _raw_stream(stream, dev)
-    x, ldx = _matrix(X, "X", shape, dt, dev)
-    y, ldy = _matrix(Y, "Y", shape, dt, dev)
-    pdt, pc = _param_dtype(X, weight, bias)
-    groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
-    w = b = mu = rs = None
-    ldw = ldb = 0
-    if weight is not None:
-        w, ldw = _params(weight, "weight", groups, K, pdt, dev)
-    if bias is not None:
-        b, ldb = _params(bias, "bias", groups, K, pdt, dev)
-    if mean is not None:
-        mu = _vector(mean, "mean", M, _F32, dev)
-    if rstd is not None:
-        rs = _vector(rstd, "rstd", M, _F32, dev)
-    rc = lib().svdq_layer_norm(code, pc, M, K, x, ldx, w, ldw, b, ldb, weight_offset,
-                               rows_per_group, eps, y, ldy, mu, rs, st)
+    rc = (_fast or _fastcall()).layer_norm(X, Y, weight, bias, eps, weight_offset, rows_per_group,
+                                           mean, rstd,
+                                           None if stream is None else stream.cuda_stream)
     if rc:
         raise SVDQError(rc, "svdq_layer_norm")
 
@@ -758,23 +755,8 @@ def svdq_rope(plan: RopePlan, positions, X, out, inverse=False, stream=None):
     head strides) into out (same shape; X itself rotates in place).
     positions: int32 [T, axes], or [R, axes] shared by tokens t with equal
     t % R.  inverse: the opposite rotation, the gradient of the first."""
-    code, dev, shape = _dtype_code(X), X.get_device(), X.shape
-    if len(shape) != 3 or out.shape != shape or out.dtype != X.dtype or out.get_device() != dev:
-        raise ValueError("X and out: expected [tokens, heads, head_dim] of one type and device")
-    T, H, D = shape
-    xt, xh, x1 = X.stride()
-    yt, yh, y1 = out.stride()
-    if D > 1 and (x1 != 1 or y1 != 1):
-        raise ValueError("X and out: a head's elements have to be contiguous")
-    axes, pshape = plan.n_axes, positions.shape
-    if len(pshape) != 2 or pshape[1] != axes or positions.dtype != _torch.int32 or \
-            positions.get_device() != dev or (axes > 1 and positions.stride(1) != 1):
-        raise ValueError(f"positions: expected int32 [rows, {axes}] on cuda:{dev}")
-    R = pshape[0]
-    ldp = positions.stride(0) if R > 1 else axes
-    st = _raw_stream(stream, dev)
-    rc = lib().svdq_rope(plan._h, code, T, H, D, positions.data_ptr(), R, ldp, X.data_ptr(), xt, xh,
-                         out.data_ptr(), yt, yh, 1 if inverse else 0, st)
+    rc = (_fast or _fastcall()).rope(plan._h.value if plan._h else 0, plan.n_axes, positions, X, out, inverse,
+                                     None if stream is None else stream.cuda_stream)
     if rc:
         raise SVDQError(rc, "svdq_rope")
 

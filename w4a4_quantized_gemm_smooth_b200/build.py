@@ -6,7 +6,8 @@ Every .cu/.cpp under csrc/ is compiled by nvcc (-gencode
 arch=compute_100a,code=sm_100a -lineinfo -O3) and linked into
 w4a4_quantized_gemm_smooth_b200/_lib/libsvdq.so.  nvcc cross-compiles; no GPU
 is needed.  Objects go to _build/ at the repository root and are rebuilt
-only when a source or header is newer.
+only when a source or header is newer.  pyext/fastcall.c becomes
+_lib/_svdq_fastcall.so, the CPython binding of the shortest calls.
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libsvdq.so")
+FASTCALL_SRC = os.path.join(PKG, "pyext", "fastcall.c")
+FASTCALL = os.path.join(LIB_DIR, "_svdq_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 HOST_FLAGS = "-fPIC,-fopenmp,-O3,-ffp-contract=off,-fno-fast-math"
@@ -85,6 +89,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stdout.write(res.stdout)
             sys.stderr.write(res.stderr)
             raise RuntimeError("link of libsvdq.so failed")
+    deps = [FASTCALL_SRC, os.path.join(INCLUDE, "svdq.h")]
+    if force or not os.path.exists(FASTCALL) or os.path.getmtime(FASTCALL) < _newest(deps):
+        cmd = ["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
+               "-I", sysconfig.get_paths()["include"], FASTCALL_SRC, "-o", FASTCALL,
+               "-L", LIB_DIR, "-lsvdq", "-Wl,-rpath,$ORIGIN"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or res.returncode != 0:
+            sys.stdout.write(res.stdout)
+            sys.stderr.write(res.stderr)
+        if res.returncode != 0:
+            raise RuntimeError("gcc failed on fastcall.c")
     return LIB
 
 
