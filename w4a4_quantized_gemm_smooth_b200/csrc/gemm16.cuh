@@ -85,6 +85,18 @@ __device__ __forceinline__ float ex2_approx(float v) {
   return r;
 }
 
+// Minimum and maximum that keep NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // For pairs: a = min(|x|, 32), e = exp(-x^2 / 2) and h = erfc(|x| / sqrt 2) / 2
 // by Abramowitz and Stegun's formula 7.1.26 (a polynomial in
 // t = 1 / (1 + 0.3275911 z) times exp(-z^2), absolute error 1.5e-7 of erfc).
@@ -96,7 +108,7 @@ struct GaussTail {
 };
 __device__ __forceinline__ GaussTail gauss_tail(float2 x) {
   GaussTail g;
-  g.a = make_float2(fminf(fabsf(x.x), 32.0f), fminf(fabsf(x.y), 32.0f));
+  g.a = make_float2(min_nan(fabsf(x.x), 32.0f), min_nan(fabsf(x.y), 32.0f));
   const float2 z = __fmul2_rn(g.a, make_float2(0.70710678f, 0.70710678f));
   const float2 d = __ffma2_rn(z, make_float2(0.3275911f, 0.3275911f), make_float2(1.0f, 1.0f));
   const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
@@ -112,28 +124,25 @@ __device__ __forceinline__ GaussTail gauss_tail(float2 x) {
 }
 
 // The activation of two sums: GELU is x (1 - h) or, for x < 0, x h, that is
-// max(x, 0) - |x| h (|x| clamped where h is 0, so that infinity stays; the
-// maximum as a sum, so that NaN stays); SiLU is x / (1 + exp(-x)).
+// max(x, 0) - |x| h (|x| clamped where h is 0, so that infinity stays); SiLU
+// is x / (1 + exp(-x)).
 __device__ __forceinline__ float2 g_act2(float2 x, int epilogue) {
   if (epilogue == SVDQ_EPI_GELU) {
     const GaussTail g = gauss_tail(x);
-    const float2 half = make_float2(0.5f, 0.5f);
-    const float2 pos = __ffma2_rn(x, half, __fmul2_rn(make_float2(fabsf(x.x), fabsf(x.y)), half));
-    return __ffma2_rn(make_float2(-g.a.x, -g.a.y), g.h, pos);
+    return __ffma2_rn(make_float2(-g.a.x, -g.a.y), g.h, make_float2(max_nan(x.x, 0.0f), max_nan(x.y, 0.0f)));
   }
   if (epilogue == SVDQ_EPI_SILU)
     return make_float2(__fdividef(x.x, 1.0f + __expf(-x.x)), __fdividef(x.y, 1.0f + __expf(-x.y)));
   return x;
 }
-// Its derivative: GELU's is Phi(x) + x phi(x).
+// Its derivative: GELU's is Phi(x) + x phi(x), with Phi = 1/2 +- (1/2 - h).
 __device__ __forceinline__ float2 g_act_grad2(float2 x, int epilogue) {
   if (epilogue == SVDQ_EPI_GELU) {
     const GaussTail g = gauss_tail(x);
-    const float2 up = make_float2(x.x < 0.0f ? g.h.x : 1.0f - g.h.x, x.y < 0.0f ? g.h.y : 1.0f - g.h.y);
+    const float2 u = __ffma2_rn(g.h, make_float2(-1.0f, -1.0f), make_float2(0.5f, 0.5f));
+    const float2 up = __fadd2_rn(make_float2(copysignf(u.x, x.x), copysignf(u.y, x.y)), make_float2(0.5f, 0.5f));
     const float2 s = make_float2(copysignf(g.a.x, x.x), copysignf(g.a.y, x.y));
-    const float2 r = __ffma2_rn(__fmul2_rn(s, make_float2(0.39894228f, 0.39894228f)), g.e, up);
-    // the clamp loses NaN
-    return make_float2(r.x + (x.x != x.x ? x.x : 0.0f), r.y + (x.y != x.y ? x.y : 0.0f));
+    return __ffma2_rn(__fmul2_rn(s, make_float2(0.39894228f, 0.39894228f)), g.e, up);
   }
   const float2 q = make_float2(__fdividef(1.0f, 1.0f + __expf(-x.x)), __fdividef(1.0f, 1.0f + __expf(-x.y)));
   return make_float2(q.x * (1.0f + x.x * (1.0f - q.x)), q.y * (1.0f + x.y * (1.0f - q.y)));

@@ -43,9 +43,9 @@ struct DpArgs {
 };
 
 // 32 columns x 8 per thread by 8 rows of threads.
-constexpr int DP_COLS = 256, DP_ROWS = 4;
+constexpr int DP_COLS = 256;
 template <int EPI>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 dp_kernel(const DpArgs a) {
   grid_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -55,37 +55,22 @@ dp_kernel(const DpArgs a) {
   const long long r1 = min((long long)a.M, r0 + a.rows_per_block);
   float2 acc[4] = {};
   auto walk = [&](auto whole) {
-    // whole: the thread's eight columns lie in the row (vector accesses).
-    // DP_ROWS rows at a time, so that their loads are in flight together.
-    constexpr bool WHOLE = decltype(whole)::value;
-    const uint16_t* dy = a.dy + c;
-    const uint16_t* pp = a.p + c;
-    uint16_t* dp = a.dp + c;
-    const int n = WHOLE ? 8 : a.N - c;
-    for (long long r = r0 + ty; r < r1; r += 8 * DP_ROWS) {
-      uint4 d4[DP_ROWS], p4[DP_ROWS];
+    // whole: the thread's eight columns lie in the row (vector accesses)
+    const int n = decltype(whole)::value ? 8 : a.N - c;
+    for (long long r = r0 + ty; r < r1; r += 8) {
+      const uint4 d4 = load8(a.dy + c + r * a.lddy, 0, n);
+      uint4 p4 = make_uint4(0, 0, 0, 0);
+      if (EPI != SVDQ_EPI_NONE) p4 = load8(a.p + c + r * a.ldp, 0, n);
+      uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+      const uint32_t pw[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-      for (int k = 0; k < DP_ROWS; ++k) {
-        d4[k] = p4[k] = make_uint4(0, 0, 0, 0);
-        if (r + 8 * k < r1) {
-          d4[k] = load8(dy + (r + 8 * k) * a.lddy, 0, n);
-          if (EPI != SVDQ_EPI_NONE) p4[k] = load8(pp + (r + 8 * k) * a.ldp, 0, n);
-        }
+      for (int e = 0; e < 4; ++e) {
+        float2 d = unpack2(dw[e], bf16);
+        if (EPI != SVDQ_EPI_NONE) d = __fmul2_rn(d, g_act_grad2(unpack2(pw[e], bf16), EPI));
+        acc[e] = __fadd2_rn(acc[e], d);
+        dw[e] = pack2(d, bf16);
       }
-#pragma unroll
-      for (int k = 0; k < DP_ROWS; ++k) {
-        uint32_t dw[4] = {d4[k].x, d4[k].y, d4[k].z, d4[k].w};
-        const uint32_t pw[4] = {p4[k].x, p4[k].y, p4[k].z, p4[k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float2 d = unpack2(dw[e], bf16);
-          if (EPI != SVDQ_EPI_NONE) d = __fmul2_rn(d, g_act_grad2(unpack2(pw[e], bf16), EPI));
-          acc[e] = __fadd2_rn(acc[e], d);
-          dw[e] = pack2(d, bf16);
-        }
-        if (EPI != SVDQ_EPI_NONE && r + 8 * k < r1)
-          store8(dp + (r + 8 * k) * a.lddp, 0, n, make_uint4(dw[0], dw[1], dw[2], dw[3]));
-      }
+      if (EPI != SVDQ_EPI_NONE) store8(a.dp + c + r * a.lddp, 0, n, make_uint4(dw[0], dw[1], dw[2], dw[3]));
     }
   };
   if (c + 8 <= a.N)
@@ -132,11 +117,12 @@ db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
   }
 }
 
-// Row blocks of dp_kernel: about four blocks per SM in all, of at least 32
+// Row blocks of dp_kernel: no more than the four blocks per SM that fit at
+// once (two more would take another round, 30 us instead of 22), of at least 32
 // rows, so that the partial sums stay small beside the rows themselves.
 int dp_row_blocks(int M, int N) {
   const int col_blocks = (int)(((long long)N + DP_COLS - 1) / DP_COLS);
-  long long b = (4 * 148 + col_blocks - 1) / col_blocks;
+  long long b = 4 * 148 / col_blocks;
   const long long most = ((long long)M + 31) / 32;
   if (b > most) b = most;
   return (int)(b < 1 ? 1 : b);
