@@ -715,3 +715,204 @@ def test_status_codes_reach_python():
         S.svdq_linear16(X, W, Y, bias=torch.zeros((7,), dtype=BF16, device="cuda"))
     with pytest.raises(ValueError):
         S.svdq_layer_norm(X, X, torch.zeros((3, 64), dtype=BF16, device="cuda"), rows_per_group=1)
+
+
+def test_chains_keep_their_order():
+    """Operators that follow one another on a stream start early but read what
+    the one before wrote; a torch kernel in between sees and changes it too."""
+    g = gen(41)
+    X0 = torch.randn((300, 1152), generator=g, device="cuda").to(BF16)
+    W = (torch.randn((1152, 1152), generator=g, device="cuda") * 1152 ** -0.5).to(BF16)
+    plan = S.svdq_rope_create([6, 6], S.rope_frequencies([6, 6]))
+    pos = torch.randint(0, 99, (300, 2), generator=g, device="cuda", dtype=torch.int32)
+
+    def chain(sync):
+        X, Y = X0.clone(), torch.empty_like(X0)
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        for i in range(12):
+            S.svdq_layer_norm(X, X)
+            wait()
+            S.svdq_linear16(X, W, Y, residual=X, epilogue=S.EPI_SILU)
+            wait()
+            X.mul_(0.5)
+            wait()
+            h = Y.unflatten(1, (48, 24))
+            S.svdq_rope(plan, pos, h, h, inverse=bool(i % 2))
+            wait()
+            S.svdq_linear16(Y[:2], W, X[1:3], residual=X[1:3])
+            wait()
+            X.add_(Y)
+            wait()
+        torch.cuda.synchronize()
+        return X
+
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
+
+
+FIRST_CAPTURED = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import w4a4_quantized_gemm_smooth_b200 as S
+dev = dict(device="cuda", dtype=torch.bfloat16)
+X, W, dY = torch.randn((200, 128), **dev), torch.randn((264, 128), **dev), torch.randn((200, 264), **dev)
+outs = lambda: [torch.empty((200, 264), **dev), torch.empty((200, 128), **dev), torch.empty((264, 128), **dev),
+                torch.empty((264,), **dev), torch.empty((200, 128), **dev), torch.empty((200, 33, 8), **dev)]
+mean, rstd = torch.empty((200,), device="cuda"), torch.empty((200,), device="cuda")
+ws = torch.empty((S.svdq_linear16_backward_workspace(200, 128, 264),), dtype=torch.uint8, device="cuda")
+pos = torch.zeros((200, 1), dtype=torch.int32, device="cuda")
+def run(o):
+    S.svdq_linear16(X, W, o[0])
+    S.svdq_linear16_backward(dY, X, W, None, o[1], o[2], o[3], ws)
+    S.svdq_layer_norm(X, o[4], mean=mean, rstd=rstd)
+    S.svdq_rope(S.svdq_rope_create([2], [1.0, 0.5]), pos, o[0].unflatten(1, (33, 8)), o[5])
+a, b = outs(), outs()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run(a)
+graph.replay()
+run(b)
+torch.cuda.synchronize()
+S.svdq_get_op_error()
+assert all(torch.equal(x, y) for x, y in zip(a, b))
+print("captured first")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURED.format(root=root)], capture_output=True, text=True,
+                       timeout=120)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_graphs_on_forked_streams():
+    """A captured fork and join: two branches with their own buffers."""
+    g = gen(42)
+    X, W = rows(g, 260, 264, BF16), rows(g, 200, 264, BF16, 0.1)
+    Y, Z, N = out(260, 200, BF16), out(260, 200, BF16), out(260, 264, BF16)
+    S.svdq_linear16(X, W, Y)
+    want = Y.clone()
+    S.svdq_layer_norm(X, N)
+    wantn = N.clone()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        with torch.cuda.stream(side):
+            S.svdq_linear16(X, W, Z)
+            S.svdq_layer_norm(X, N)
+        S.svdq_linear16(X, W, Y)
+        cur.wait_stream(side)
+        Y.add_(Z)
+    for _ in range(3):
+        Y.zero_(), Z.zero_(), N.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Z, want) and torch.equal(N, wantn) and torch.equal(Y, want + want)
+
+
+# ------------------------------------------- the paths of the quantised layers
+def _packed(K, N, rank, seed):
+    import synth
+    L = synth.make_layer(synth.layer_spec(f"ops16_{K}_{N}", 64, K, N, rank, seed, tiny=True))
+    return S.svdq_pack_weights(L.W, S.svdq_calib_absmax(L.X), rank, bias_bits=L.b)
+
+
+def test_qkv_path():
+    """Modulated norm, W4A4 QKV product, rotation of its queries and keys:
+    the same bits as the calls one by one; the values are not touched."""
+    g = gen(51)
+    M, K, heads, kv, D = 150, 256, 4, 2, 32
+    w = _packed(K, (heads + 2 * kv) * D, 16, 7)
+    scale, shift = (rows(g, 3, K, BF16, 0.3) for _ in range(2))
+    X = rows(g, M, K, BF16)
+    pos = torch.randint(0, 60, (50, 3), generator=g, device="cuda", dtype=torch.int32)
+    plan = S.svdq_rope_create([4, 6, 6], S.rope_frequencies([4, 6, 6]))
+    path = S.SVDQQKV(w, heads, D, plan, S.LayerNorm(scale, shift, weight_offset=1.0), kv_heads=kv)
+    Y = path.forward(X, pos, rows_per_group=50).clone()
+    N = torch.empty((M, K), dtype=BF16, device="cuda")
+    S.svdq_layer_norm(X, N, scale, shift, weight_offset=1.0, rows_per_group=50)
+    P = S.SVDQLinear(w)(N)
+    qk = P[:, :(heads + kv) * D].unflatten(1, (-1, D))
+    R = torch.empty_like(qk)
+    S.svdq_rope(plan, pos, qk, R)
+    torch.cuda.synchronize()
+    S.svdq_get_device_error(w)
+    assert torch.equal(Y[:, :(heads + kv) * D], R.flatten(1))
+    assert torch.equal(Y[:, (heads + kv) * D:], P[:, (heads + kv) * D:])
+    with pytest.raises(ValueError):
+        S.SVDQQKV(w, heads, D + 8, plan)
+    w.free()
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_mlp_path_with_norm(fused):
+    g = gen(52)
+    fc1, fc2 = _packed(256, 512, 16, 8), _packed(512, 256, 16, 9)
+    X = rows(g, 100, 256, BF16)
+    norm = S.LayerNorm(torch.rand((256,), generator=g, device="cuda") + 0.5)
+    Y = S.SVDQMLP(fc1, fc2, norm).forward(X, fused=fused).clone()
+    N = torch.empty((100, 256), dtype=BF16, device="cuda")
+    S.svdq_layer_norm(X, N, norm.weight)
+    Z = S.SVDQMLP(fc1, fc2).forward(N, fused=fused)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Z)
+    fc1.free()
+    fc2.free()
+
+
+def test_a_block_of_them_eager_and_captured():
+    """norm, QKV and rotation, a 16-bit projection of the values added to the
+    residual stream, norm, MLP: each step against the 64-bit form of its own
+    input, then the whole as a graph, bit for bit."""
+    g = gen(53)
+    M, C, heads, D = 200, 256, 8, 32
+    qkv, fc1, fc2 = _packed(C, 3 * C, 16, 1), _packed(C, 512, 16, 2), _packed(512, C, 16, 3)
+    plan = S.svdq_rope_create([4, 12], S.rope_frequencies([4, 12]), S.ROPE_HALVES)
+    pos = torch.randint(0, 64, (M, 2), generator=g, device="cuda", dtype=torch.int32)
+    X = rows(g, M, C, BF16)
+    Wo, bo = rows(g, C, C, BF16, C ** -0.5), torch.randn((C,), generator=g, device="cuda").to(BF16)
+    attn = S.SVDQQKV(qkv, heads, D, plan, S.LayerNorm())
+    proj, mlp = S.Linear16(Wo, bo), S.SVDQMLP(fc1, fc2, S.LayerNorm())
+    H, Yo = torch.empty_like(X.contiguous()), torch.empty((M, C), dtype=BF16, device="cuda")
+
+    def block():
+        Q = attn(X, pos)
+        proj(Q[:, 2 * C:], residual=X, out=H)
+        return Q, mlp(H, out=Yo)
+
+    Q, Y = (t.clone() for t in block())
+    h = half(BF16)
+    # the normed input and the product's rows before the rotation
+    N = torch.empty((M, C), dtype=BF16, device="cuda")
+    S.svdq_layer_norm(X, N)
+    x, _, _, _, y0, _, _, _ = norm64(X, None, None, 1e-6, 0.0, 0)
+    close(N, y0, (h + 2.0 ** -14) * (y0.abs() + 2.0 ** -14), "norm")
+    P = S.SVDQLinear(qkv)(N)
+    ref, mag = rope64(P[:, :2 * C].unflatten(1, (2 * heads, D)), pos, [4, 12], S.rope_frequencies([4, 12]),
+                      S.ROPE_HALVES, False)
+    close(Q[:, :2 * C].unflatten(1, (2 * heads, D)), ref, h * (ref.abs() + 2.0 ** -21 * mag) + 2.0 ** -21 * mag, "rope")
+    v, wo = P[:, 2 * C:].double(), Wo.double()
+    ref = v @ wo.T + bo.double() + X.double()
+    e = (C + 2) * 2.0 ** -24 * (v.abs() @ wo.abs().T + bo.double().abs() + X.double().abs())
+    close(H, ref, h * (ref.abs() + e) + e, "projection")
+    N2 = torch.empty((M, C), dtype=BF16, device="cuda")
+    S.svdq_layer_norm(H, N2)
+    assert torch.equal(Y, S.SVDQMLP(fc1, fc2)(N2))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        Qc, Yc = block()
+    Qc.zero_(), Yc.zero_(), H.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Qc, Q) and torch.equal(Yc, Y)
+    for w in (qkv, fc1, fc2):
+        w.free()

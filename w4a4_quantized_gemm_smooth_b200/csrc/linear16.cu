@@ -118,12 +118,12 @@ db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
 }
 
 // Row blocks of dp_kernel: no more than the four blocks per SM that fit at
-// once (two more would take another round, 30 us instead of 22), of at least 32
+// once (two more would take another round, 30 us instead of 22), of at least 16
 // rows, so that the partial sums stay small beside the rows themselves.
 int dp_row_blocks(int M, int N) {
   const int col_blocks = (int)(((long long)N + DP_COLS - 1) / DP_COLS);
   long long b = 4 * 148 / col_blocks;
-  const long long most = ((long long)M + 31) / 32;
+  const long long most = ((long long)M + 15) / 16;
   if (b > most) b = most;
   return (int)(b < 1 ? 1 : b);
 }
