@@ -485,22 +485,8 @@ def svdq_debug_partials(w: Weights, M, xq, row0, nrows, col0, ncols, P, stream=N
 # 16-bit operators around the quantised layers.  These calls take plain
 # tensors, so the binding checks each one's device, type and shape before it
 # passes the pointer on (ValueError); the library checks sizes and alignment.
-
-# The three calls that one token makes (svdq_linear16, svdq_layer_norm and
-# svdq_rope) make the same checks in a small CPython module, since a call
-# through ctypes takes the host longer than the device.
-
-_torch = None
-_DTYPES: dict = {}
-_F32 = None
-
-
-def _load_torch():
-    global _torch, _F32
-    import torch
-    _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    _torch, _F32 = torch, torch.float32
-
+# They go through a small CPython module, since a call through ctypes takes
+# the host longer than one token's kernels take the device.
 
 _fast = None
 
@@ -511,6 +497,7 @@ def _fastcall():
     global _fast
     if _fast is None:
         import importlib.util
+        import torch
         lib()
         path = os.path.join(_PKG, "_lib", "_svdq_fastcall.so")
         if not os.path.exists(path):
@@ -520,63 +507,10 @@ def _fastcall():
         spec = importlib.util.spec_from_file_location("_svdq_fastcall", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
-        import torch
         mod.init((torch.bfloat16, torch.float16, torch.float32), torch.int32,
                  torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         _fast = mod
     return _fast
-
-
-def _dtype_code(t, name="X"):
-    if _torch is None:
-        _load_torch()
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name}: dtype {t.dtype} is not supported")
-    return code
-
-
-def _raw_stream(stream, dev):
-    """The stream's handle; None: the current stream of device `dev` (the
-    tensors' one), which has to be the current device: launches go there."""
-    if dev < 0:
-        raise ValueError("the tensors have to be on a CUDA device")
-    if dev != _torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream
-
-
-def _matrix(t, name, shape, dtype, dev):
-    """(pointer, leading dimension) of a tensor of this shape (two sizes) and
-    type on device `dev`, with contiguous rows."""
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype or t.get_device() != dev:
-        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype} on cuda:{dev}")
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: rows have to be contiguous")
-    if shape[0] <= 1:
-        ld = -(-shape[1] // 8) * 8          # a single row has no pitch
-    return t.data_ptr(), ld
-
-
-def _vector(t, name, n, dtype, dev):
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected {n} contiguous values")
-    if t.dtype != dtype or t.get_device() != dev:
-        raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {dtype} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _opt_workspace(ws, dev):
-    if ws is None:
-        return None, 0
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def svdq_linear16(X, W, Y, bias=None, residual=None, epilogue=EPI_NONE, preact=None, stream=None):
@@ -599,66 +533,16 @@ def svdq_linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue=
     """Gradients of svdq_linear16: dX [M, K], dW [N, K] and dbias [N] (each may
     be None) for dY [M, N]; preact is the forward call's (None without an
     activation).  The residual's gradient is dY itself."""
-    code, dev, dt = _dtype_code(dY, "dY"), dY.get_device(), dY.dtype
-    M, N = dY.shape
-    if X is None and W is None:
-        K = 1                       # only dbias is wanted
-    else:
-        K = (X if X is not None else W).shape[1]
-    st = _raw_stream(stream, dev)
-    d, ldd = _matrix(dY, "dY", (M, N), dt, dev)
-    x = w = p = gx = gw = gb = None
-    ldx = ldw = ldp = ldgx = ldgw = 0
-    if X is not None:
-        x, ldx = _matrix(X, "X", (M, K), dt, dev)
-    if W is not None:
-        w, ldw = _matrix(W, "W", (N, K), dt, dev)
-    if preact is not None:
-        p, ldp = _matrix(preact, "preact", (M, N), dt, dev)
-    if dX is not None:
-        gx, ldgx = _matrix(dX, "dX", (M, K), dt, dev)
-    if dW is not None:
-        gw, ldgw = _matrix(dW, "dW", (N, K), dt, dev)
-    if dbias is not None:
-        gb = _vector(dbias, "dbias", N, dt, dev)
-    ws, nbytes = _opt_workspace(workspace, dev)
-    _check(lib().svdq_linear16_backward(code, M, K, N, d, ldd, x, ldx, w, ldw, p, ldp, epilogue,
-                                        gx, ldgx, gw, ldgw, gb, ws, nbytes, st),
-           "svdq_linear16_backward")
+    rc = (_fast or _fastcall()).linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue,
+                                                  None if stream is None else stream.cuda_stream)
+    if rc:
+        raise SVDQError(rc, "svdq_linear16_backward")
 
 
 def svdq_get_op_error(stream=None):
     """Synchronises the stream and raises if a bounded wait of a 16-bit
     operator expired on the current device since the last call."""
     _check(lib().svdq_get_op_error(_stream_ptr(stream)), "device")
-
-
-def _params(t, name, groups, K, dtype, dev, shared=True):
-    """(pointer, leading dimension) of a parameter [groups, K] or [K] (shared
-    by every group); a gradient (not shared) has a row per group."""
-    shape = t.shape
-    if shape == (K,) or shape == (1, K):
-        if not shared and groups != 1:
-            raise ValueError(f"{name}: expected [{groups}, {K}]")
-        ld = 0 if shared else -(-K // 8) * 8
-    elif shape == (groups, K):
-        ld = t.stride(0)
-    else:
-        raise ValueError(f"{name}: expected [{groups}, {K}] or [{K}]")
-    if t.get_device() != dev or t.dtype != dtype or (t.stride()[-1] != 1 and K > 1):
-        raise ValueError(f"{name}: expected contiguous rows of {dtype} on cuda:{dev}")
-    return t.data_ptr(), ld
-
-
-def _param_dtype(X, *ps):
-    """The parameters' common type (X's type or float32) and its code."""
-    for p in ps:
-        if p is not None:
-            code = _DTYPES.get(p.dtype)
-            if code is None:
-                raise ValueError(f"parameters: dtype {p.dtype} is not supported")
-            return p.dtype, code
-    return X.dtype, _DTYPES[X.dtype]
 
 
 def svdq_layer_norm(X, Y, weight=None, bias=None, eps=1e-6, weight_offset=0.0, rows_per_group=0,
@@ -684,29 +568,11 @@ def svdq_layer_norm_backward(dY, X, mean, rstd, dX, weight=None, weight_offset=0
                              stream=None):
     """Gradients of svdq_layer_norm: dX [M, K] (may be dY or X), dweight and
     dbias [groups, K] or, with one group, [K]; each may be None."""
-    code, dev, dt, shape = _dtype_code(X), X.get_device(), X.dtype, X.shape
-    M, K = shape
-    st = _raw_stream(stream, dev)
-    d, ldd = _matrix(dY, "dY", shape, dt, dev)
-    x, ldx = _matrix(X, "X", shape, dt, dev)
-    pdt, pc = _param_dtype(X, weight, dweight, dbias)
-    groups = -(-M // rows_per_group) if rows_per_group > 0 else 1
-    gx = w = gw = gb = None
-    ldgx = ldw = ldgw = ldgb = 0
-    if dX is not None:
-        gx, ldgx = _matrix(dX, "dX", shape, dt, dev)
-    if weight is not None:
-        w, ldw = _params(weight, "weight", groups, K, pdt, dev)
-    if dweight is not None:
-        gw, ldgw = _params(dweight, "dweight", groups, K, pdt, dev, False)
-    if dbias is not None:
-        gb, ldgb = _params(dbias, "dbias", groups, K, pdt, dev, False)
-    mu = _vector(mean, "mean", M, _F32, dev)
-    rs = _vector(rstd, "rstd", M, _F32, dev)
-    ws, nbytes = _opt_workspace(workspace, dev)
-    _check(lib().svdq_layer_norm_backward(code, pc, M, K, d, ldd, x, ldx, mu, rs, w, ldw,
-                                          weight_offset, rows_per_group, gx, ldgx, gw, ldgw, gb,
-                                          ldgb, ws, nbytes, st), "svdq_layer_norm_backward")
+    rc = (_fast or _fastcall()).layer_norm_backward(dY, X, mean, rstd, dX, weight, weight_offset,
+                                                    rows_per_group, dweight, dbias, workspace,
+                                                    None if stream is None else stream.cuda_stream)
+    if rc:
+        raise SVDQError(rc, "svdq_layer_norm_backward")
 
 
 class RopePlan:

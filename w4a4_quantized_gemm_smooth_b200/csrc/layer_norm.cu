@@ -618,8 +618,11 @@ int split_rows(int M, int rows_per_group, int per_sm, int rows) {
   return (int)(s < 1 ? 1 : s);
 }
 // Backward: at least eight rows per block (two per warp of a four-warp
-// block), so that the partial sums stay a small share of the traffic.
-int bwd_splits(int M, int rows_per_group) { return split_rows(M, rows_per_group, 2, 8); }
+// block), so that the partial sums stay a small share of the traffic; a group
+// of up to 16 rows is one block, whose sums are final (no second launch).
+int bwd_splits(int M, int rows_per_group) {
+  return M <= 16 || rows_per_group <= 16 ? 1 : split_rows(M, rows_per_group, 2, 8);
+}
 
 // Raises the kernel's dynamic shared-memory limit once per device.
 template <typename K>

@@ -36,7 +36,8 @@ struct DpArgs {
   const uint16_t* dy;
   const uint16_t* p;       // pre-activation, null without an activation
   uint16_t* dp;            // null without an activation
-  float* part;             // [row blocks][N8] column sums, or null
+  float* part;             // [row blocks][N] column sums, or null
+  uint16_t* db;            // [N], for a single row block, or null
   long long lddy, ldp, lddp;
   int M, N, rows_per_block;
   int bf16;
@@ -77,7 +78,7 @@ dp_kernel(const DpArgs a) {
     walk(std::true_type());
   else if (c < a.N)
     walk(std::false_type());
-  if (!a.part) return;
+  if (!a.part && !a.db) return;
   __shared__ float sh[8][DP_COLS + 8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -90,7 +91,10 @@ dp_kernel(const DpArgs a) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += sh[i][threadIdx.x];
-    a.part[(size_t)blockIdx.y * a.N + col] = s;
+    if (a.part)
+      a.part[(size_t)blockIdx.y * a.N + col] = s;
+    else
+      a.db[col] = (uint16_t)pack2(make_float2(s, 0.0f), bf16);
   }
 }
 
@@ -119,8 +123,10 @@ db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
 
 // Row blocks of dp_kernel: no more than the four blocks per SM that fit at
 // once (two more would take another round, 30 us instead of 22), of at least 16
-// rows, so that the partial sums stay small beside the rows themselves.
+// rows, so that the partial sums stay small beside the rows themselves; a
+// small batch is one block, whose sums are db itself (no second launch).
 int dp_row_blocks(int M, int N) {
+  if (M <= 64) return 1;
   const int col_blocks = (int)(((long long)N + DP_COLS - 1) / DP_COLS);
   long long b = 4 * 148 / col_blocks;
   const long long most = ((long long)M + 15) / 16;
@@ -316,16 +322,19 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
       dP = d.dp;
       lddp = L.lddp;
     }
-    if (db) d.part = reinterpret_cast<float*>(base + L.part);
     const int want = svdq::dp_row_blocks(M, N);
     d.rows_per_block = (int)(((long long)M + want - 1) / want);
     const int blocks = (int)(((long long)M + d.rows_per_block - 1) / d.rows_per_block);
     const dim3 grid((unsigned)(((long long)N + svdq::DP_COLS - 1) / svdq::DP_COLS), (unsigned)blocks);
+    if (db && blocks == 1)
+      d.db = static_cast<uint16_t*>(db);
+    else if (db)
+      d.part = reinterpret_cast<float*>(base + L.part);
     auto kernel = epilogue == SVDQ_EPI_GELU   ? svdq::dp_kernel<SVDQ_EPI_GELU>
                   : epilogue == SVDQ_EPI_SILU ? svdq::dp_kernel<SVDQ_EPI_SILU>
                                               : svdq::dp_kernel<SVDQ_EPI_NONE>;
     if (svdq::launch_op(kernel, grid, 256, 0, 1, stream, d) != cudaSuccess) return SVDQ_ERR_CUDA;
-    if (db && svdq::launch_op(svdq::db_join_kernel, dim3((unsigned)(((long long)N + 31) / 32)), 1024, 0,
+    if (d.part && svdq::launch_op(svdq::db_join_kernel, dim3((unsigned)(((long long)N + 31) / 32)), 1024, 0,
                               1, stream, d.part, blocks, N, static_cast<uint16_t*>(db),
                               bf16) != cudaSuccess)
       return SVDQ_ERR_CUDA;

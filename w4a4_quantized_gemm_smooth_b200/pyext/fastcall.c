@@ -1,9 +1,8 @@
 /*
- * The binding of the three 16-bit operators whose calls may be shorter than
- * their marshalling: one token's layer norm runs 2.5 us on the device, and the
- * ctypes call with its checks in Python took 4.7 us of the host beside the
- * launch; this takes about 1.5.  Argument marshalling and checks only (the
- * same as the package's Python code makes for the other calls); the work is
+ * The binding of the 16-bit operators, whose calls may be shorter than their
+ * marshalling: one token's layer norm runs 2.5 us on the device, and a ctypes
+ * call with its checks in Python took 4.7 us of the host beside the launch;
+ * this takes about 1.5.  Argument marshalling and checks only; the work is
  * libsvdq.so's.  Uses the CPython API and the tensors' Python attributes.
  */
 #define PY_SSIZE_T_CLEAN
@@ -11,7 +10,7 @@
 
 #include "svdq.h"
 
-static PyObject *s_shape, *s_dtype, *s_stride, *s_data_ptr, *s_get_device;
+static PyObject *s_shape, *s_dtype, *s_stride, *s_data_ptr, *s_get_device, *s_is_contiguous, *s_nbytes;
 static PyObject *g_dtypes[3];              /* torch.bfloat16, .float16, .float32 */
 static PyObject *g_int32, *g_device, *g_raw_stream;
 
@@ -261,6 +260,124 @@ static PyObject *layer_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
+/* A workspace (contiguous, any type), or None. */
+static int read_workspace(PyObject *o, int dev, void **ptr, size_t *bytes) {
+  PyObject *v;
+  *ptr = NULL;
+  *bytes = 0;
+  if (o == Py_None) return 0;
+  if (!(v = PyObject_CallMethodNoArgs(o, s_get_device))) return -1;
+  const long d = PyLong_AsLong(v);
+  Py_DECREF(v);
+  if (!(v = PyObject_CallMethodNoArgs(o, s_is_contiguous))) return -1;
+  const int whole = PyObject_IsTrue(v);
+  Py_DECREF(v);
+  if (PyErr_Occurred()) return -1;
+  if (d != dev || !whole) {
+    PyErr_Format(PyExc_ValueError, "workspace: expected a contiguous tensor on cuda:%d", dev);
+    return -1;
+  }
+  if (!(v = PyObject_GetAttr(o, s_nbytes))) return -1;
+  *bytes = PyLong_AsSize_t(v);
+  Py_DECREF(v);
+  if (PyErr_Occurred() || !(v = PyObject_CallMethodNoArgs(o, s_data_ptr))) return -1;
+  *ptr = PyLong_AsVoidPtr(v);
+  Py_DECREF(v);
+  return PyErr_Occurred() ? -1 : 0;
+}
+
+/* linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue, stream) -> status */
+static PyObject *linear16_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  Tensor d, t;
+  void *x, *w, *p, *gx, *gw, *gb, *ws;
+  int ldd, ldx, ldw, ldp, ldgx, ldgw;
+  size_t bytes;
+  cudaStream_t st;
+  svdq_status rc;
+  if (!nargs_are(n, 10) || read_tensor(a[0], "dY", &d) < 0 || check_dtype(&d, "dY") < 0 ||
+      read_sizes(&d, "dY") < 0 || read_stream(a[9], d.dev, &st) < 0)
+    return NULL;
+  const long long M = d.shape[0], N = d.shape[1];
+  long long K = 1;                         /* only dbias is wanted */
+  PyObject *const with_k = a[1] != Py_None ? a[1] : a[2];
+  if (with_k != Py_None) {
+    if (read_tensor(with_k, "X, W", &t) < 0 || read_sizes(&t, "X, W") < 0) return NULL;
+    K = t.shape[1];
+  }
+  const long epi = PyLong_AsLong(a[8]);
+  if (epi == -1 && PyErr_Occurred()) return NULL;
+  if (N > 1 && d.stride[1] != 1) {
+    PyErr_SetString(PyExc_ValueError, "dY: rows have to be contiguous");
+    return NULL;
+  }
+  ldd = pitch(M <= 1 ? (N + 7) / 8 * 8 : d.stride[0]);
+  if (read_matrix(a[1], "X", M, K, &d, &x, &ldx) < 0 || read_matrix(a[2], "W", N, K, &d, &w, &ldw) < 0 ||
+      read_matrix(a[3], "preact", M, N, &d, &p, &ldp) < 0 ||
+      read_matrix(a[4], "dX", M, K, &d, &gx, &ldgx) < 0 ||
+      read_matrix(a[5], "dW", N, K, &d, &gw, &ldgw) < 0 ||
+      read_vector(a[6], "dbias", N, d.code, d.dev, &gb) < 0 ||
+      read_workspace(a[7], d.dev, &ws, &bytes) < 0)
+    return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  rc = svdq_linear16_backward(d.code, (int)M, (int)K, (int)N, d.ptr, ldd, x, ldx, w, ldw, p, ldp, (int)epi,
+                              gx, ldgx, gw, ldgw, gb, ws, bytes, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* layer_norm_backward(dY, X, mean, rstd, dX, weight, weight_offset, rows_per_group, dweight, dbias,
+ *                     workspace, stream) -> status */
+static PyObject *layer_norm_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  Tensor x;
+  void *d, *mu, *rs, *gx, *w, *gw, *gb, *ws;
+  int ldx, ldd, ldgx, ldw, ldgw, ldgb, pc = -1;
+  size_t bytes;
+  cudaStream_t st;
+  svdq_status rc;
+  if (!nargs_are(n, 12) || read_tensor(a[1], "X", &x) < 0 || check_dtype(&x, "X") < 0 ||
+      read_sizes(&x, "X") < 0 || read_stream(a[11], x.dev, &st) < 0)
+    return NULL;
+  const long long M = x.shape[0], K = x.shape[1];
+  const double off = PyFloat_AsDouble(a[6]);
+  const long long rpg = PyLong_AsLongLong(a[7]);
+  if (PyErr_Occurred()) return NULL;
+  if (rpg > 0x7FFFFFFF || rpg < -0x7FFFFFFF) {
+    PyErr_SetString(PyExc_ValueError, "rows_per_group: expected less than 2^31");
+    return NULL;
+  }
+  if (K > 1 && x.stride[1] != 1) {
+    PyErr_SetString(PyExc_ValueError, "X: rows have to be contiguous");
+    return NULL;
+  }
+  ldx = pitch(M <= 1 ? (K + 7) / 8 * 8 : x.stride[0]);
+  const long long groups = rpg > 0 ? (M + rpg - 1) / rpg : 1;
+  if (a[0] == Py_None || a[2] == Py_None || a[3] == Py_None) {
+    PyErr_SetString(PyExc_ValueError, "dY, mean and rstd: expected tensors");
+    return NULL;
+  }
+  if (read_matrix(a[0], "dY", M, K, &x, &d, &ldd) < 0 ||
+      read_vector(a[2], "mean", M, SVDQ_DTYPE_F32, x.dev, &mu) < 0 ||
+      read_vector(a[3], "rstd", M, SVDQ_DTYPE_F32, x.dev, &rs) < 0 ||
+      read_matrix(a[4], "dX", M, K, &x, &gx, &ldgx) < 0 ||
+      read_param(a[5], "weight", groups, K, x.dev, &pc, &w, &ldw) < 0 ||
+      read_param(a[8], "dweight", groups, K, x.dev, &pc, &gw, &ldgw) < 0 ||
+      read_param(a[9], "dbias", groups, K, x.dev, &pc, &gb, &ldgb) < 0 ||
+      read_workspace(a[10], x.dev, &ws, &bytes) < 0)
+    return NULL;
+  /* a gradient has a row per group: one row is all of them only for one group */
+  if ((gw && ldgw == 0 && groups != 1) || (gb && ldgb == 0 && groups != 1)) {
+    PyErr_Format(PyExc_ValueError, "dweight, dbias: expected %lld rows", groups);
+    return NULL;
+  }
+  if (gw && ldgw == 0) ldgw = pitch((K + 7) / 8 * 8);
+  if (gb && ldgb == 0) ldgb = pitch((K + 7) / 8 * 8);
+  Py_BEGIN_ALLOW_THREADS
+  rc = svdq_layer_norm_backward(x.code, pc < 0 ? x.code : pc, (int)M, (int)K, d, ldd, x.ptr, ldx, mu, rs, w,
+                                ldw, (float)off, (int)rpg, gx, ldgx, gw, ldgw, gb, ldgb, ws, bytes, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
 /* rope(plan handle, axes, positions, X, out, inverse, stream) -> status */
 static PyObject *rope(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   Tensor p, x, y;
@@ -315,6 +432,8 @@ static PyObject *init(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyMethodDef methods[] = {
     {"init", (PyCFunction)(void (*)(void))init, METH_FASTCALL, NULL},
     {"linear16", (PyCFunction)(void (*)(void))linear16, METH_FASTCALL, NULL},
+    {"linear16_backward", (PyCFunction)(void (*)(void))linear16_backward, METH_FASTCALL, NULL},
+    {"layer_norm_backward", (PyCFunction)(void (*)(void))layer_norm_backward, METH_FASTCALL, NULL},
     {"layer_norm", (PyCFunction)(void (*)(void))layer_norm, METH_FASTCALL, NULL},
     {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
@@ -328,6 +447,8 @@ PyMODINIT_FUNC PyInit__svdq_fastcall(void) {
   s_stride = PyUnicode_InternFromString("stride");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_get_device = PyUnicode_InternFromString("get_device");
-  if (!s_shape || !s_dtype || !s_stride || !s_data_ptr || !s_get_device) return NULL;
+  s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+  s_nbytes = PyUnicode_InternFromString("nbytes");
+  if (!s_is_contiguous || !s_nbytes || !s_shape || !s_dtype || !s_stride || !s_data_ptr || !s_get_device) return NULL;
   return PyModule_Create(&module);
 }
