@@ -323,7 +323,8 @@ def check_norm(M, K, dtype, pt, groups=1, off=0.0, affine=True, offset=0.0, seed
     close(rs, rstd[:, 0], (rstd * (e_r + u))[:, 0], "rstd")
 
 
-SIZES = [(1, 1), (1, 2), (3, 7), (5, 8), (2, 63), (4, 64), (7, 255), (129, 256), (130, 257), (33, 768), (6, 1152),
+SHORT = [(1001, 68), (777, 119), (4099, 40), (515, 16), (2050, 128), (333, 130), (1500, 256)]
+SIZES = SHORT + [(1, 1), (1, 2), (3, 7), (5, 8), (2, 63), (4, 64), (7, 255), (129, 256), (130, 257), (33, 768), (6, 1152),
          (1000, 1152), (9, 1281), (40, 2049), (20, 3073), (17, 4608), (5, 5121), (3, 8193), (2, 12288), (2, 16384)]
 
 
@@ -333,7 +334,8 @@ def test_norm_sizes(M, K, dtype, pt):
     check_norm(M, K, dtype, pt, seed=M + K)
 
 
-@pytest.mark.parametrize("M,K,groups", [(8, 72, 8), (10, 1152, 3), (1000, 136, 4), (7, 4608, 7), (5, 520, 2)])
+@pytest.mark.parametrize("M,K,groups", [(8, 72, 8), (10, 1152, 3), (1000, 136, 4), (7, 4608, 7), (5, 520, 2),
+                                        (103, 24, 13), (1001, 60, 3), (999, 125, 2)])
 @pytest.mark.parametrize("off", [0.0, 1.0])
 def test_norm_groups(M, K, groups, off):
     check_norm(M, K, BF16, BF16, groups, off, seed=K)
@@ -429,7 +431,7 @@ def test_norm_backward_sizes(M, K, dtype, pt):
 
 
 @pytest.mark.parametrize("M,K,groups", [(8, 72, 8), (10, 1152, 3), (1000, 136, 4), (7, 4608, 7), (2000, 520, 2),
-                                        (1100, 1153, 5)])
+                                        (1100, 1153, 5), (103, 24, 13), (1001, 60, 3), (999, 125, 2)])
 @pytest.mark.parametrize("off", [0.0, 1.0])
 def test_norm_backward_groups(M, K, groups, off):
     check_norm_bwd(M, K, BF16, BF16, groups, off, seed=K)

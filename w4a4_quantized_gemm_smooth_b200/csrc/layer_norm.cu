@@ -1,7 +1,8 @@
 // Layer norm with a scale and a shift per group of rows, and its gradients.
 //
-// A row belongs to one team (a warp, or a block of 128 or 512 threads for
-// long rows), and a team walks over rows of one group, two at a time.  Each
+// A row belongs to one team (a quarter of a warp for the shortest rows, a
+// warp, or a block of 128 or 512 threads for long ones), and a team walks over
+// rows of one group, two or four at a time.  Each
 // thread copies its own 16-byte vectors of the next rows to its own places in
 // shared memory (cp.async, no barrier), so that the bytes in flight do not
 // depend on the registers that a row needs; the group's scale (with its
@@ -57,19 +58,23 @@ __device__ __forceinline__ RowSpan block_span(int M, int rows_per_group, int spl
 }
 
 // How a row of up to G NV V elements (V = 16 / sizeof(T)) is held: threads of
-// a block, teams of a block, rows at a time and in flight per team, and whether the scale
-// and shift are kept in shared memory (not for the longest rows, which need
-// the room; they are read from the caches).
+// a block, teams of a block and of a warp, rows at a time and in flight per
+// team, blocks per SM, and whether the scale and shift are kept in shared
+// memory (not for the longest rows, which need the room; they are read from
+// the caches).
 template <typename T, int G, int NV>
 struct NormCfg {
   static constexpr int V = 16 / (int)sizeof(T), H = V / 2;
   static constexpr int THREADS = G > 128 ? G : 128;
   static constexpr int TEAMS = THREADS / G;
+  static constexpr int TW = G < 32 ? 32 / G : 1;
   static constexpr bool PSMEM = G < 512;
-  static constexpr int RF = G < 512 ? 2 : 1;                   // rows at a time, forward
+  static constexpr int RF = NV == 1 ? 4 : G < 512 ? 2 : 1;     // rows at a time, forward
   static constexpr int DF = 2;                                 // and steps in flight
-  static constexpr int RB = G < 512 ? 2 : 1;                   // backward (x and dy): rows at a time
+  static constexpr int RB = RF;                                // backward (x and dy): rows at a time
   static constexpr int DB = NV < 8 ? 2 : 1;                    // and steps in flight
+  static constexpr int SM_F = NV == 1 ? 6 : G < 512 ? 4 : 1;   // blocks per SM
+  static constexpr int SM_B = NV == 1 ? 4 : G < 512 ? 2 : 1;
   static constexpr size_t PARAM = PSMEM ? (size_t)NV * G * V * 4 : 0;   // one fp32 row
   static constexpr size_t RING_FWD = (size_t)DF * RF * NV * THREADS * 16;
   static constexpr size_t RING_BWD = (size_t)DB * RB * 2 * NV * THREADS * 16;
@@ -152,45 +157,63 @@ __device__ __forceinline__ void read_param(float2 (&out)[V / 2], const float4* s
   }
 }
 
-// Sums over a team of G threads (G = 32: the warp; else the whole block) of
-// R values (1, 2 or 4) that every thread then has.  Inside a warp the values
-// are scattered over the lanes while they are summed, which takes 4 to 6
-// exchanges instead of 5 R.  `red` has room for R G / 32 values; successive
-// calls alternate between two of them, so that one barrier per call is enough.
+// Sums over a team of G threads (G <= 32: part of a warp, or the warp; else
+// the whole block) of R values that every thread then has.  In a whole warp up
+// to four values are scattered over the lanes while they are summed, which
+// takes 4 to 6 exchanges instead of 5 R.  `red` has room for R G / 32 values;
+// successive calls alternate between two of them, so that one barrier per
+// call is enough.
 template <int G, int R>
 __device__ __forceinline__ void team_sum(float (&v)[R], float* red) {
-  const int lane = threadIdx.x & 31;
-  float c;
-  if constexpr (R == 4) {
-    const bool h = lane & 16;
-    float a = h ? v[2] : v[0], b = h ? v[3] : v[1];
-    a += __shfl_xor_sync(0xFFFFFFFFu, h ? v[0] : v[2], 16);
-    b += __shfl_xor_sync(0xFFFFFFFFu, h ? v[1] : v[3], 16);
-    const bool g = lane & 8;
-    c = (g ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, g ? a : b, 8);
-  } else if constexpr (R == 2) {
-    const bool h = lane & 16;
-    c = (h ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, h ? v[0] : v[1], 16);
-    c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
+  if constexpr (G < 32) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  } else if constexpr (R == 8) {
+    static_assert(G == 32, "rows of four at a time have one vector per thread");
+    float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+    team_sum<G, 4>(a, red);
+    team_sum<G, 4>(b, red);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = a[k];
+      v[4 + k] = b[k];
+    }
   } else {
-    c = v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
-    c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
-  }
+    const int lane = threadIdx.x & 31;
+    float c;
+    if constexpr (R == 4) {
+      const bool h = lane & 16;
+      float a = h ? v[2] : v[0], b = h ? v[3] : v[1];
+      a += __shfl_xor_sync(0xFFFFFFFFu, h ? v[0] : v[2], 16);
+      b += __shfl_xor_sync(0xFFFFFFFFu, h ? v[1] : v[3], 16);
+      const bool g = lane & 8;
+      c = (g ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, g ? a : b, 8);
+    } else if constexpr (R == 2) {
+      const bool h = lane & 16;
+      c = (h ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, h ? v[0] : v[1], 16);
+      c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
+    } else {
+      c = v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
+      c += __shfl_xor_sync(0xFFFFFFFFu, c, 8);
+    }
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-  constexpr int L = 32 / R;                  // lanes that hold one value
-  if constexpr (G == 32) {
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+    constexpr int L = 32 / R;                  // lanes that hold one value
+    if constexpr (G == 32) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, c, k * L);
-  } else {
-    constexpr int W = G / 32;
-    if (lane % L == 0) red[(lane / L) * W + (threadIdx.x >> 5)] = c;
-    __syncthreads();
+      for (int k = 0; k < R; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, c, k * L);
+    } else {
+      constexpr int W = G / 32;
+      if (lane % L == 0) red[(lane / L) * W + (threadIdx.x >> 5)] = c;
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      v[k] = 0.0f;
+      for (int k = 0; k < R; ++k) {
+        v[k] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[k] += red[k * W + i];
+        for (int i = 0; i < W; ++i) v[k] += red[k * W + i];
+      }
     }
   }
 }
@@ -204,7 +227,7 @@ __device__ __forceinline__ float sum_pairs(const float2 (&a)[H]) {
 }
 
 template <typename T, typename PT, int G, int NV>
-__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 4 : 1)
+__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, NormCfg<T, G, NV>::SM_F)
 norm_kernel(const NormArgs p) {
   using C = NormCfg<T, G, NV>;
   constexpr int V = C::V, H = C::H, D = C::DF, TH = C::THREADS, R = C::RF;
@@ -244,8 +267,11 @@ norm_kernel(const NormArgs p) {
   const float inv_k = 1.0f / (float)p.K;
   const bool ragged = p.K % V != 0;
   int slot = 0;
-  // R rows at a time: their sums overlap, and the parameters are read once
-  for (long long row = span.r0 + team * R; row < span.r1; row += C::TEAMS * R) {
+  // R rows at a time: their sums overlap, and the parameters are read once.
+  // The teams of a warp step together (they exchange sums), as long as the
+  // first of them has a row.
+  const int behind = (team % C::TW) * R;
+  for (long long row = span.r0 + team * R; row - behind < span.r1; row += C::TEAMS * R) {
     cp_async_wait<D - 1>();
     float2 v[R][NV][H];
     float sum[R], rstd[R], mu[R];
@@ -321,7 +347,7 @@ norm_kernel(const NormArgs p) {
             const float2 t = w ? __fmul2_rn(r2, fw[j]) : r2;
             o.set(j, b ? __ffma2_rn(v[k][i][j], t, fb[j]) : __fmul2_rn(v[k][i][j], t));
           }
-          if (k == 0 || row + k < span.r1)
+          if ((k == 0 && C::TW == 1) || row + k < span.r1)
             store_vec<T, V>(y + k * p.ldy, c, i + 1 < NV ? INT_MAX : p.K, o);
         }
       }
@@ -350,7 +376,7 @@ struct NormBwdArgs {
 
 // PARAMS: dweight or dbias is wanted.
 template <typename T, typename PT, int G, int NV, bool PARAMS>
-__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, G < 512 ? 2 : 1)
+__global__ void __launch_bounds__(NormCfg<T, G, NV>::THREADS, NormCfg<T, G, NV>::SM_B)
 norm_bwd_kernel(const NormBwdArgs p) {
   using C = NormCfg<T, G, NV>;
   constexpr int V = C::V, H = C::H, D = C::DB, TH = C::THREADS, TEAMS = C::TEAMS, R = C::RB;
@@ -370,6 +396,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
   if constexpr (C::PSMEM)
     if (w) sw.load(w, p.K);
   float nmu[D][R], nrs[D][R];                // the statistics of the rows in flight
+  const int behind = (team % C::TW) * R;     // as in the forward kernel
   auto fetch = [&](long long row, int slot) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -377,7 +404,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
       if (row + k < span.r1) {
         share.fetch(x + (row + k) * p.ldx, lane, ring_u + at * 16, TH * 16);
         share.fetch(dy + (row + k) * p.lddy, lane, ring_u + (at + NV * TH) * 16, TH * 16);
-      } else if (k > 0 && row < span.r1) {   // a step's missing row adds nothing
+      } else if (row - behind < span.r1) {   // a step's missing row adds nothing
         share.clear(ring + at, TH);
         share.clear(ring + at + NV * TH, TH);
       }
@@ -411,7 +438,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
   }
   int slot = 0, phase = 0;
   // R rows at a time: their sums overlap, and the scale is read once
-  for (long long row = span.r0 + team * R; row < span.r1; row += TEAMS * R) {
+  for (long long row = span.r0 + team * R; row - behind < span.r1; row += TEAMS * R) {
     cp_async_wait<D - 1>();
     const uint4* q = ring + slot * R * 2 * NV * TH;
     float2 m[R], r[R], s1[R], s2[R];
@@ -489,7 +516,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
               const float2 t = w ? __fmul2_rn(g, f[j]) : g;
               o.set(j, __ffma2_rn(t, r[k], __ffma2_rn(__fmul2_rn(d, r[k]), s2[k], s1[k])));
             }
-            if (k == 0 || row + k < span.r1)
+            if ((k == 0 && C::TW == 1) || row + k < span.r1)
               store_vec<T, V>(dx + k * p.lddx, c, i + 1 < NV ? INT_MAX : p.K, o);
           }
         }
@@ -620,8 +647,10 @@ int split_rows(int M, int rows_per_group, int per_sm, int rows) {
 // Backward: at least eight rows per block (two per warp of a four-warp
 // block), so that the partial sums stay a small share of the traffic; a group
 // of up to 16 rows is one block, whose sums are final (no second launch).
-int bwd_splits(int M, int rows_per_group) {
-  return M <= 16 || rows_per_group <= 16 ? 1 : split_rows(M, rows_per_group, 2, 8);
+// The split does not depend on the element type (the workspace's size does
+// not know it): rows of up to 256 elements have the more blocks per SM.
+int bwd_splits(int M, int K, int rows_per_group) {
+  return M <= 16 || rows_per_group <= 16 ? 1 : split_rows(M, rows_per_group, K <= 256 ? 4 : 2, 8);
 }
 
 // Raises the kernel's dynamic shared-memory limit once per device.
@@ -643,7 +672,7 @@ cudaError_t fwd_launch(NormArgs a, cudaStream_t st) {
   const cudaError_t e = allow_smem(norm_kernel<T, PT, G, NV>, C::FWD_SMEM, done);
   if (e != cudaSuccess) return e;
   const long long groups = ((long long)a.M + a.rows_per_group - 1) / a.rows_per_group;
-  a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : 4, C::TEAMS);
+  a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : C::SM_F, C::TEAMS);
   return launch_op(norm_kernel<T, PT, G, NV>, dim3((unsigned)(groups * a.splits)), C::THREADS,
                    C::FWD_SMEM, 1, st, a);
 }
@@ -653,6 +682,8 @@ cudaError_t fwd_launch(NormArgs a, cudaStream_t st) {
 // so that only a thread's last vector can lie past it.
 template <int V, typename F>
 cudaError_t dispatch_row(int vecs, F&& f) {
+  if (vecs <= 8 * 1) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+  if (vecs <= 16 * 1) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
   if (vecs <= 32 * 1) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
   if (vecs <= 32 * 2) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
   if (vecs <= 32 * 3) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 3>());
@@ -768,7 +799,7 @@ size_t svdq_layer_norm_backward_workspace(int M, int K, int rows_per_group) {
   if (M <= 0 || K < 1 || K > SVDQ_NORM_MAX_K || rows_per_group < 0) return 0;
   const int rpg = rows_per_group ? rows_per_group : M;
   const size_t groups = ((size_t)M + rpg - 1) / rpg;
-  const int s = svdq::bwd_splits(M, rpg);
+  const int s = svdq::bwd_splits(M, K, rpg);
   return s == 1 ? 0 : groups * s * 2 * (size_t)svdq::part_pitch(K) * sizeof(float);
 }
 
@@ -804,7 +835,7 @@ svdq_status svdq_layer_norm_backward(int dtype, int param_dtype, int M, int K, c
   if (!dX && !dweight && !dbias) return SVDQ_OK;
   svdq::NormBwdArgs a{};
   a.rows_per_group = rows_per_group ? rows_per_group : M;
-  a.splits = svdq::bwd_splits(M, a.rows_per_group);
+  a.splits = svdq::bwd_splits(M, K, a.rows_per_group);
   const size_t need = (dweight || dbias) ? svdq_layer_norm_backward_workspace(M, K, rows_per_group) : 0;
   if (need) {
     if (!workspace) return SVDQ_ERR_INVALID_ARG;
