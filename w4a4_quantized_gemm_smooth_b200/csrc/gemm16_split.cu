@@ -9,6 +9,11 @@
 // up its share of the columns over the CTAs, in rank order, and runs the
 // epilogue on it.  No workspace, no atomics, one launch.
 //
+// An SM takes 64 bytes a cycle from L2, so a 128 x 128 tile's stage (32 KB)
+// lasts 0.26 us whatever the tensor cores do, and a launch with one stage 4 to
+// 6 us.  333 x 1153 to 2307 (fp16, GELU, residual, pre-activation): 9.8 us as
+// 111 tiles of 128 x 64; 128 x 12288 to 1152: 16 us split by 8, 58 unsplit.
+//
 // 10 warps: TMA, MMA (and TMEM), eight epilogue warps.
 #include "elem.cuh"
 #include "gemm16.cuh"

@@ -12,12 +12,18 @@
 //
 // Forward: the variance is the two-pass one, sum (x - mu)^2 in fp32 after the
 // mean, from registers (no cancellation for rows with a large mean).
+// 16384 x 1152 bf16 in four groups: 17.0 us, 4.4 TB/s (a plain copy: 13.7 us);
+// bound by the chain sum - difference - sum - output of the few rows that fit
+// an SM's registers at a time.
 //
 // Backward: a thread owns fixed columns; their sums of dy xhat and dy stay in
 // its registers over all the rows of the team and are joined at the end:
 // teams of a block in shared memory, blocks of a group through fp32 partials
 // in the workspace, summed in block order by a second kernel.  X and dY are
-// read once.
+// read once.  16384 x 1152 bf16: 28.3 us, 4.0 TB/s; 4608 x 4608 fp16: 32.9 us,
+// 3.9 TB/s.  The columns' sums take the registers that more rows would need;
+// two warps per row instead of one (48 sums a thread instead of 80) measured
+// the same, so did one row at a time with three blocks per SM.
 #include <climits>
 #include <cmath>
 #include <type_traits>

@@ -31,7 +31,9 @@ int* op_err_address() {
 namespace {
 
 // ------------------------------------------------ activation's gradient
-// dP = dY epi'(P) rounded to 16 bits, and the column sums of its fp32 values.
+// dP = dY epi'(P) rounded to 16 bits (the operand type of the products that
+// follow), and the column sums of its fp32 values.  Bound by memory: 4096 x
+// 4608 with GELU 23 us with its join, 4.9 TB/s.
 struct DpArgs {
   const uint16_t* dy;
   const uint16_t* p;       // pre-activation, null without an activation

@@ -7,8 +7,11 @@
 // (2^-32 turn) go through sincospi.  A far position thus costs no accuracy.
 //
 // Bound by memory: one read and one write of T H D elements.  A thread holds
-// the sines and cosines of one vector's pairs and walks the heads, so the
-// trigonometry is paid once per heads_per_thread heads.
+// the sines and cosines of one vector's pairs and walks the heads, four loads
+// at a time, so the trigonometry is paid once per heads_per_thread heads.
+// 4608 tokens x 64 heads x 128 (bf16, in rows of 12288): 28.4 us, 5.3 TB/s;
+// 16640 x 32 x 72 in halves (fp16, 8-byte vectors): 29.8 us, 5.2 TB/s; a plain
+// copy of as many bytes takes 25 us.
 #include <cmath>
 #include <new>
 
