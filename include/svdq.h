@@ -659,8 +659,9 @@ void svdq_rope_free(svdq_rope_plan* plan);
  * plan's pairs; elements past the pairs are copied.  At most
  * SVDQ_ROPE_MAX_HEADS heads of SVDQ_ROPE_MAX_HEAD_DIM elements, else
  * SVDQ_ERR_UNSUPPORTED.  Pointers and strides need only element alignment
- * (16-byte aligned ones are faster).  Heads and tokens of Y do not share
- * elements; Y may be X with equal strides (in place).  positions: device int32 [pos_rows][ld_pos], one
+ * (16-byte aligned ones are faster).  In Y all heads lie within a token's
+ * stride or all tokens within a head's (else SVDQ_ERR_SHAPE); Y may be X with
+ * equal strides (in place).  positions: device int32 [pos_rows][ld_pos], one
  * column per axis, any sign; token t uses row t % pos_rows (images of one
  * size in a batch share their positions).  Queries and keys side by side in
  * the rows of a fused QKV product are one call over their heads.

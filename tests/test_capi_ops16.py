@@ -29,6 +29,7 @@ def test_linear16_refusals():
     assert linear(ldx=56) == SHAPE and linear(ldw=56) == SHAPE and linear(ldy=24) == SHAPE
     assert linear(R=D, ldr=24) == SHAPE and linear(P=D, ldp=24) == SHAPE
     assert linear(M=0x7FFFFFFF) == UNSUPPORTED
+    assert linear(K=0x7FFF8000, ldx=0x7FFF8000, ldw=0x7FFF8000) == UNSUPPORTED
     for k in ("X", "W", "Y"):
         assert linear(**{k: None}) == INVALID
         assert linear(**{k: 0x10008}) == ALIGN
@@ -151,6 +152,9 @@ def test_rope_refusals():
     assert rope(D=126) == SHAPE and rope(D=129, yh=129) == SHAPE and rope(D=0) == SHAPE
     assert rope(xt=-1) == SHAPE and rope(xh=-1) == SHAPE and rope(yt=-1) == SHAPE and rope(yh=-1) == SHAPE
     assert rope(yh=64) == SHAPE and rope(yt=64) == SHAPE         # heads or tokens of Y overlap
+    assert rope(yt=200) == SHAPE and rope(H=3, yt=256, yh=130) == SHAPE
+    assert rope(T=1, yt=0, X=0x10001) == ALIGN and rope(H=1, yh=0, X=0x10001) == ALIGN   # a single one has no stride
+    assert rope(yh=1000, yt=128, X=0x10001) == ALIGN             # tokens within a head
     assert rope(D=1026, yh=1026, yt=4000) == UNSUPPORTED and rope(H=65536) == UNSUPPORTED
     assert rope(pos=None) == INVALID and rope(X=None) == INVALID and rope(Y=None) == INVALID
     assert rope(X=B, Y=B, yt=512) == INVALID                     # in place with other strides

@@ -117,6 +117,15 @@ def test_linear_sizes(M, K, N, dtype):
     check_linear(M, K, N, dtype, S.EPI_GELU, seed=M + K + N)
 
 
+@pytest.mark.parametrize("M,K,N", [
+    (20, 2696, 1599), (133, 2640, 2583), (92, 2866, 5), (137, 1606, 1297), (132, 2764, 1236), (424, 5, 2475),
+    (128, 12288, 1152), (60, 9000, 300), (700, 1000, 4000)])
+def test_linear_forms(M, K, N):
+    """Sizes for which the other tile widths and splits are chosen."""
+    check_linear(M, K, N, BF16, S.EPI_GELU, seed=K)
+    check_linear(M, K, N, F16, S.EPI_NONE, bias=False, pre=False, seed=K)
+
+
 @pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
 @pytest.mark.parametrize("K,N", [(1, 1), (8, 4736), (250, 4737), (4096, 33), (4097, 5000), (8200, 50), (12287, 129)])
 def test_linear_few_rows(M, K, N):
@@ -236,6 +245,12 @@ def check_linear_bwd(M, K, N, dtype, epi, bias=True, seed=0, want=(True, True, T
 @pytest.mark.parametrize("epi", [S.EPI_NONE, S.EPI_GELU, S.EPI_SILU])
 def test_linear_backward(M, K, N, dtype, epi):
     check_linear_bwd(M, K, N, dtype, epi, seed=M)
+
+
+@pytest.mark.parametrize("M,K,N", [(5, 2712, 668), (535, 5, 469), (100, 198, 2980), (198, 5, 693), (203, 68, 2488),
+                                   (65, 40, 300), (64, 40, 300)])
+def test_linear_backward_forms(M, K, N):
+    check_linear_bwd(M, K, N, BF16, S.EPI_SILU, seed=K)
 
 
 @pytest.mark.parametrize("M,K,N,dtype", [(4096, 1152, 1160, BF16), (9000, 136, 400, F16)])

@@ -176,6 +176,7 @@ gemm16_split_kernel(const __grid_constant__ G16Problem p0, const __grid_constant
         const int col = n0 + 32 * (c0 + c) + lane;
         bias_s[32 * c + lane] = p.bias && col < p.N ? unpack2(__ldg(p.bias + col), p.bf16 != 0).x : 0.0f;
       }
+      __syncwarp();
     }
     bool alive = g_wait(tm_full, 0, abort_flag, err);
     // also after an expired wait: the residual's boxes land before the CTA ends

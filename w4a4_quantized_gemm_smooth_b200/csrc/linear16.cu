@@ -223,9 +223,9 @@ BwdLayout bwd_layout(int M, int N, int epilogue) {
   return L;
 }
 
-// Row and column indexes of a last, partial tile stay below 2^31.
+// Indexes of a last, partial tile (of up to 4096 elements) stay below 2^31.
 bool sizes_fit(int M, int K, int N) {
-  constexpr int most = 0x7FFFFC00;
+  constexpr int most = 0x7FFF0000;
   return M <= most && K <= most && N <= most;
 }
 

@@ -292,9 +292,14 @@ svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int hea
   if (head_dim > SVDQ_ROPE_MAX_HEAD_DIM || heads > SVDQ_ROPE_MAX_HEADS) return SVDQ_ERR_UNSUPPORTED;
   if (tokens == 0 || heads == 0) return SVDQ_OK;
   if (!positions || !X || !Y) return SVDQ_ERR_INVALID_ARG;
-  // two heads or tokens never share an element of Y
-  const long long hd = head_dim;
-  if ((heads > 1 && ldy_head < hd) || (tokens > 1 && ldy_token < hd)) return SVDQ_ERR_SHAPE;
+  // two heads or tokens never share an element of Y: all heads lie within a
+  // token's stride, or all tokens within a head's
+  const __int128 hd = head_dim;
+  const bool in_token = (heads == 1 || ldy_head >= hd) &&
+                        (tokens == 1 || ldy_token >= (__int128)(heads - 1) * ldy_head + hd);
+  const bool in_head = (tokens == 1 || ldy_token >= hd) &&
+                       (heads == 1 || ldy_head >= (__int128)(tokens - 1) * ldy_token + hd);
+  if (!in_token && !in_head) return SVDQ_ERR_SHAPE;
   if (X == Y && ((tokens > 1 && ldx_token != ldy_token) || (heads > 1 && ldx_head != ldy_head)))
     return SVDQ_ERR_INVALID_ARG;
   const uintptr_t e = dtype == SVDQ_DTYPE_F32 ? 3 : 1;
