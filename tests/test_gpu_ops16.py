@@ -126,8 +126,8 @@ def test_linear_forms(M, K, N):
     check_linear(M, K, N, F16, S.EPI_NONE, bias=False, pre=False, seed=K)
 
 
-@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
-@pytest.mark.parametrize("K,N", [(1, 1), (8, 4736), (250, 4737), (4096, 33), (4097, 5000), (8200, 50), (12287, 129)])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17])
+@pytest.mark.parametrize("K,N", [(1, 1), (31, 9), (32, 8), (250, 4737), (4097, 33), (1153, 5000), (12287, 129)])
 def test_linear_few_rows(M, K, N):
     for dtype in (BF16, F16):
         check_linear(M, K, N, dtype, S.EPI_SILU, seed=M + K)

@@ -418,10 +418,9 @@ inline bool make_problem(G16Problem* p, const Operand& A, const Operand& B, cons
 cudaError_t launch_gemm16_pair(const G16Launch& l, int bn, cudaStream_t st);
 cudaError_t launch_gemm16_split(const G16Launch& l, int bn, int splits, cudaStream_t st);
 
-// The forward product of a few rows on the CUDA cores, where it is the
-// faster form.
-bool gemv16_fits(int M, int K, int N);
-cudaError_t launch_gemv16(const void* X, long long ldx, const void* W, long long ldw, int K,
+// The forward product of up to THIN_ROWS rows, bound by reading W.
+constexpr int THIN_ROWS = 16;
+cudaError_t launch_thin16(const void* X, long long ldx, const void* W, long long ldw, int K,
                           const G16Out& o, cudaStream_t st);
 
 }  // namespace svdq

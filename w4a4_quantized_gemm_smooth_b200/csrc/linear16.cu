@@ -269,8 +269,8 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
   o.bf16 = l.bf16;
   o.M = M;
   o.N = N;
-  if (svdq::gemv16_fits(M, K, N))
-    return svdq::launch_gemv16(X, ldx, W, ldw, K, o, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  if (M <= svdq::THIN_ROWS)
+    return svdq::launch_thin16(X, ldx, W, ldw, K, o, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
   return svdq::launch_gemm(l, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
 }
 
