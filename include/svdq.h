@@ -528,9 +528,10 @@ svdq_status svdq_linear_nvfp4(const svdq_weights* w, int M, const uint8_t* xq,
  *     other output except where stated;
  *   - calls are asynchronous on `stream`, allocate nothing and may be
  *     captured into a graph; a kernel may be brought up while the one before
- *     it on the stream runs out, and touches memory once that has finished; a workspace is needed only while its call runs,
- *     and calls that share one must not overlap (graphs that were captured
- *     with the same workspace included);
+ *     it on the stream runs out, and touches memory once that has finished;
+ *     a workspace is needed only while its call runs, and calls that share
+ *     one must not overlap (graphs that were captured with the same workspace
+ *     included);
  *   - sums, statistics and activations are fp32, outputs are rounded once.
  * ------------------------------------------------------------------------
  */

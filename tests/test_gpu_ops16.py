@@ -206,6 +206,41 @@ def test_linear_extreme_activations():
         assert bool(y[13].isnan()) or float(y[13]) == 0.0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M", [8, 40, 3000])
+def test_linear_activation_tails(dtype, M):
+    """Activations and slopes far on the negative side, where they are tiny,
+    keep their relative accuracy: the products here are exact, so a value may
+    be off by its rounding, by 2^-15 of itself (the Gaussian tail's form and
+    its exponential's argument, up to 90, in fp32) and by what fp32 cannot hold.
+    Phi is taken from erfc: 1 + erf, which ndtr computes, cancels here (at -7 it
+    keeps three digits of 64 bits)."""
+    Phi = lambda p: torch.special.erfc(-p * 0.5 ** 0.5) / 2
+    phi = lambda p: torch.exp(-p * p / 2) / (2 * torch.pi) ** 0.5
+    g = gen(M)
+    v = (-14.0 * torch.rand((M, 1), generator=g, device="cuda")).to(dtype)
+    X = torch.zeros((M, 8), dtype=dtype, device="cuda")
+    X[:, :1] = v
+    W = torch.zeros((8, 8), dtype=dtype, device="cuda")
+    W[:, 0] = 1.0
+    h, tiny = half(dtype), 16 * 2.0 ** -126 + (2.0 ** -25 if dtype == F16 else 0.0)
+    for epi in (S.EPI_GELU, S.EPI_SILU):
+        Y = out(M, 8, dtype)
+        S.svdq_linear16(X, W, Y, epilogue=epi)
+        ref = v.double() * Phi(v.double()) if epi == S.EPI_GELU else act64(v.double(), epi)
+        assert bool(((Y.double() - ref).abs() <= (h + 2.0 ** -15) * ref.abs() + tiny).all())
+        # one row's db is its dP: the slopes along 8 M columns
+        P = v.reshape(1, -1).contiguous()
+        db = torch.empty((M,), dtype=dtype, device="cuda")
+        ws = torch.empty((S.svdq_linear16_backward_workspace(1, 8, M, epi),), dtype=torch.uint8, device="cuda")
+        S.svdq_linear16_backward(torch.ones_like(P), None, None, P, None, None, db, ws, epi)
+        p = P[0].double()
+        ref = Phi(p) + p * phi(p) if epi == S.EPI_GELU else act_grad64(p, epi)
+        # the slope's two terms cancel in part: the errors are theirs
+        parts = Phi(p) + p.abs() * phi(p) if epi == S.EPI_GELU else torch.sigmoid(p) * (1 + p.abs())
+        assert bool(((db.double() - ref).abs() <= h * ref.abs() + 2.0 ** -15 * parts + tiny).all())
+
+
 def check_linear_bwd(M, K, N, dtype, epi, bias=True, seed=0, want=(True, True, True)):
     g = gen(seed)
     X, W = rows(g, M, K, dtype), rows(g, N, K, dtype, K ** -0.5)

@@ -98,11 +98,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // For pairs: a = min(|x|, 32), e = exp(-x^2 / 2) and h = erfc(|x| / sqrt 2) / 2
-// by Abramowitz and Stegun's formula 7.1.26 (a polynomial in
-// t = 1 / (1 + 0.3275911 z) times exp(-z^2), absolute error 1.5e-7 of erfc).
-// The epilogue's erff costs as much as the products of a short reduction;
-// this form is a third of it, and its error (8e-8 of |x|) is far below a
-// 16-bit step.
+// as e times a polynomial in t = 1 / (1 + z / 2), z = |x| / sqrt 2.  Its
+// coefficients are a minimax fit (a linear program over z <= 9.4, where e
+// leaves fp32) of the larger of the absolute error over 1e-7 and the relative
+// one over 2e-5; in fp32 h is off by at most 2e-7 and by 1.5e-5 of itself, so
+// that also the far negative side, where GELU is x h, is right to its own
+// 16-bit step.  The epilogue's erff costs as much as the products of a short
+// reduction; this form is a third of it.
 struct GaussTail {
   float2 a, e, h;
 };
@@ -110,15 +112,17 @@ __device__ __forceinline__ GaussTail gauss_tail(float2 x) {
   GaussTail g;
   g.a = make_float2(min_nan(fabsf(x.x), 32.0f), min_nan(fabsf(x.y), 32.0f));
   const float2 z = __fmul2_rn(g.a, make_float2(0.70710678f, 0.70710678f));
-  const float2 d = __ffma2_rn(z, make_float2(0.3275911f, 0.3275911f), make_float2(1.0f, 1.0f));
+  const float2 d = __ffma2_rn(z, make_float2(0.5f, 0.5f), make_float2(1.0f, 1.0f));
   const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
   const float2 q = __fmul2_rn(__fmul2_rn(g.a, make_float2(-0.72134752f, -0.72134752f)), g.a);
   g.e = make_float2(ex2_approx(q.x), ex2_approx(q.y));
-  auto c = [](float v) { return make_float2(0.5f * v, 0.5f * v); };
-  float2 p = __ffma2_rn(t, c(1.061405429f), c(-1.453152027f));
-  p = __ffma2_rn(p, t, c(1.421413741f));
-  p = __ffma2_rn(p, t, c(-0.284496736f));
-  p = __ffma2_rn(p, t, c(0.254829592f));
+  auto c = [](float v) { return make_float2(v, v); };
+  float2 p = __ffma2_rn(t, c(0.0436265685f), c(-0.175381176f));
+  p = __ffma2_rn(p, t, c(0.188301504f));
+  p = __ffma2_rn(p, t, c(0.0251118732f));
+  p = __ffma2_rn(p, t, c(0.13775973f));
+  p = __ffma2_rn(p, t, c(0.139472375f));
+  p = __ffma2_rn(p, t, c(0.141109165f));
   g.h = __fmul2_rn(__fmul2_rn(p, t), g.e);
   return g;
 }
@@ -135,12 +139,12 @@ __device__ __forceinline__ float2 g_act2(float2 x, int epilogue) {
     return make_float2(__fdividef(x.x, 1.0f + __expf(-x.x)), __fdividef(x.y, 1.0f + __expf(-x.y)));
   return x;
 }
-// Its derivative: GELU's is Phi(x) + x phi(x), with Phi = 1/2 +- (1/2 - h).
+// Its derivative: GELU's is Phi(x) + x phi(x), with Phi = 1 - h, or h for x < 0.
 __device__ __forceinline__ float2 g_act_grad2(float2 x, int epilogue) {
   if (epilogue == SVDQ_EPI_GELU) {
     const GaussTail g = gauss_tail(x);
-    const float2 u = __ffma2_rn(g.h, make_float2(-1.0f, -1.0f), make_float2(0.5f, 0.5f));
-    const float2 up = __fadd2_rn(make_float2(copysignf(u.x, x.x), copysignf(u.y, x.y)), make_float2(0.5f, 0.5f));
+    const float2 u = __ffma2_rn(g.h, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+    const float2 up = make_float2(x.x < 0.0f ? g.h.x : u.x, x.y < 0.0f ? g.h.y : u.y);
     const float2 s = make_float2(copysignf(g.a.x, x.x), copysignf(g.a.y, x.y));
     return __ffma2_rn(__fmul2_rn(s, make_float2(0.39894228f, 0.39894228f)), g.e, up);
   }
