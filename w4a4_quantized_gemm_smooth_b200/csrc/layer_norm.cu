@@ -650,13 +650,18 @@ int split_rows(int M, int rows_per_group, int per_sm, int rows) {
   if (s > most) s = most;
   return (int)(s < 1 ? 1 : s);
 }
-// Backward: at least eight rows per block (two per warp of a four-warp
-// block), so that the partial sums stay a small share of the traffic; a group
-// of up to 16 rows is one block, whose sums are final (no second launch).
-// The split does not depend on the element type (the workspace's size does
-// not know it): rows of up to 256 elements have the more blocks per SM.
+// Backward: rows of up to 1280 elements, of which a block has several teams,
+// in blocks of at least eight (300 x 1152: 6.1 us, 7.0 with four), a group of
+// up to 16 in one, whose sums are final (16 x 200: 3.1 us, 4.4 with a second
+// launch).  Longer rows, at which the whole block works, in blocks of at least
+// two (64 x 4608: 7.1 us, 10.9 with eight; 16 x 12288: 12, 37 in one), a group
+// of up to four in one.  The split does not depend on the element type (the
+// workspace's size does not know it): rows of up to 256 elements have four
+// blocks per SM (60000 x 256: 23 us, 33 with two).
 int bwd_splits(int M, int K, int rows_per_group) {
-  return M <= 16 || rows_per_group <= 16 ? 1 : split_rows(M, rows_per_group, K <= 256 ? 4 : 2, 8);
+  const int len = M < rows_per_group ? M : rows_per_group;
+  if (len <= (K <= 1280 ? 16 : 4)) return 1;
+  return split_rows(M, rows_per_group, K <= 256 ? 4 : 2, K <= 1280 ? 8 : 2);
 }
 
 // Raises the kernel's dynamic shared-memory limit once per device.

@@ -124,14 +124,16 @@ db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
 }
 
 // Row blocks of dp_kernel: no more than the four blocks per SM that fit at
-// once (two more would take another round, 30 us instead of 22), of at least 16
-// rows, so that the partial sums stay small beside the rows themselves; a
-// small batch is one block, whose sums are db itself (no second launch).
+// once (two more would take another round, 30 us instead of 22), of at least
+// eight rows (gradients of 128 x 1152 to 4608: 29.4 us, 30.4 with 16, 36 with
+// 64); a batch of up to 32 rows is one block, whose sums are db itself (no
+// second launch: 32 x 512 to 512 7.8 us, 8.0 with two; 64 x 1152 to 4608 34 us
+// in one block, 28.9 in eight).
 int dp_row_blocks(int M, int N) {
-  if (M <= 64) return 1;
+  if (M <= 32) return 1;
   const int col_blocks = (int)(((long long)N + DP_COLS - 1) / DP_COLS);
   long long b = 4 * 148 / col_blocks;
-  const long long most = ((long long)M + 15) / 16;
+  const long long most = ((long long)M + 7) / 8;
   if (b > most) b = most;
   return (int)(b < 1 ? 1 : b);
 }

@@ -50,9 +50,6 @@ __device__ __forceinline__ void sincos_turn(int32_t pos, uint64_t turn, bool inv
 constexpr int ROPE_THREADS = 256;
 constexpr int ROPE_BATCH = 4;      // heads whose loads are in flight together
 
-// V elements per vector.  HALVES: a unit below rot_units holds pairs
-// [V unit, V unit + V) as two vectors P elements apart, a later unit one
-// vector past the pairs; interleaved: a unit is one vector.
 // V elements of a head, of any alignment; pairs of them as fp32.
 template <typename T, int V, int ALIGN>
 struct alignas(ALIGN) RopeVec {
@@ -184,10 +181,14 @@ cudaError_t launch_v(const RopeTurns& t, RopeArgs a, int tokens, int head_dim, c
     a.units = head_dim / V;
   }
   a.work = (long long)tokens * a.units;
-  // Heads per thread: as many as 8 while the grid still covers the GPU with
-  // a thousand threads per SM; small batches spread the heads instead.
+  // Heads per thread: 8 while that leaves 64 threads per SM; smaller batches
+  // spread the heads instead, down to one a thread.  The trigonometry of a
+  // vector costs as much as several heads: 1024 tokens x 32 x 72 take 5.0 us
+  // with 8 heads a thread and 7.6 with 2; 16 tokens 2.7 with 8 and 2.1 with 1;
+  // 4608 x 64 x 128 27.5 with 8, 42.8 with 4 and 26.1 with 16, with which
+  // 2048 x 32 x 128 takes 11.8 instead of 9.7.
   int hpt = 8;
-  while (hpt > 1 && a.work * ((a.heads + hpt - 1) / hpt) < 148 * 1024) hpt >>= 1;
+  while (hpt > 1 && a.work * ((a.heads + hpt - 1) / hpt) < 148 * 64) hpt >>= 1;
   a.heads_per_thread = hpt;
   const long long blocks = (a.work + ROPE_THREADS - 1) / ROPE_THREADS;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
