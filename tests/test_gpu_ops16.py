@@ -274,6 +274,47 @@ def check_linear_bwd(M, K, N, dtype, epi, bias=True, seed=0, want=(True, True, T
         close(db, ref, h * (ref.abs() + e) + e, "db")
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 16, 17])
+@pytest.mark.parametrize("K,N", [(1, 1), (7, 300), (64, 4737), (131, 33), (1153, 700), (4097, 65), (9000, 20)])
+def test_linear_backward_few_rows(M, K, N):
+    for dtype, epi in ((BF16, S.EPI_SILU), (F16, S.EPI_GELU), (BF16, S.EPI_NONE)):
+        check_linear_bwd(M, K, N, dtype, epi, seed=M + N)
+
+
+@pytest.mark.parametrize("M", [1, 8, 16])
+def test_linear_backward_few_rows_replayed(M):
+    """Captured and replayed on other contents, on another stream: the same bits as a plain call."""
+    g = gen(M)
+    K, N = 1153, 2001
+    X, W, dY, P = rows(g, M, K, BF16), rows(g, N, K, BF16), rows(g, M, N, BF16), rows(g, M, N, BF16)
+    dX, dW, db = out(M, K, BF16), out(N, K, BF16), torch.empty((N,), dtype=BF16, device="cuda")
+    ws = torch.empty((S.svdq_linear16_backward_workspace(M, K, N, S.EPI_GELU),), dtype=torch.uint8, device="cuda")
+    call = lambda: S.svdq_linear16_backward(dY, X, W, P, dX, dW, db, ws, S.EPI_GELU)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    X.copy_(rows(g, M, K, BF16))
+    dY.copy_(rows(g, M, N, BF16))
+    call()
+    want = [t.clone() for t in (dX, dW, db)]
+    for _ in range(3):
+        for t in (dX, dW, db, ws):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((dX, dW, db), want))
+
+
+@pytest.mark.parametrize("want", [(True, False, False), (False, True, False), (False, False, True), (True, False, True),
+                                  (False, True, True)])
+@pytest.mark.parametrize("M", [1, 7, 16])
+def test_linear_backward_few_rows_parts(M, want):
+    for epi in (S.EPI_NONE, S.EPI_GELU):
+        check_linear_bwd(M, 650, 1001, BF16, epi, seed=4, want=want)
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 200, 136), (2, 65, 7), (33, 72, 300), (64, 64, 64), (129, 130, 131),
                                    (333, 1153, 77), (777, 200, 1001), (1000, 1152, 320)])
 @pytest.mark.parametrize("dtype", [BF16, F16])

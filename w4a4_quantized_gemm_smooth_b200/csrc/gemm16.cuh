@@ -427,4 +427,19 @@ constexpr int THIN_ROWS = 16;
 cudaError_t launch_thin16(const void* X, long long ldx, const void* W, long long ldw, int K,
                           const G16Out& o, cudaStream_t st);
 
+// The gradients of up to THIN_BWD_ROWS rows: x and dw, w and dx are null together.
+constexpr int THIN_BWD_ROWS = 8;
+struct ThinBwdCall {
+  const void *dy, *p, *x, *w;
+  void *dx, *dw, *db, *workspace;
+  long long lddy, ldp, ldx, ldw, lddx, lddw;
+  int M, K, N, epilogue, bf16;
+};
+size_t thin16_bwd_workspace(int M, int K, int N);
+cudaError_t launch_thin16_bwd(const ThinBwdCall& c, cudaStream_t st);
+
+// out [rows][ldo] = the sums over `blocks` of part [block][rows][pitch], in order.
+cudaError_t launch_join(const float* part, int blocks, int rows, int cols, int pitch, uint16_t* out,
+                        long long ldo, int bf16, cudaStream_t st);
+
 }  // namespace svdq

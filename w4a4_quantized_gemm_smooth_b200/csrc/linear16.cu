@@ -8,7 +8,8 @@
 // axis is contiguous in memory is K-major; one whose other axis is, is
 // MN-major: TMA brings both as 128-byte-swizzled boxes, and the MMA's
 // descriptors say which way they lie, so no transposed copy is ever made.
-// Both gradients go out in one launch.
+// Both gradients go out in one launch where one form suits both.  Few rows go
+// another way (thin16.cu, thin16_bwd.cu).
 #include "elem.cuh"
 #include "gemm16.cuh"
 
@@ -100,26 +101,31 @@ dp_kernel(const DpArgs a) {
   }
 }
 
-// db = the row blocks' sums in order: 32 columns by 32 rows of threads, each
-// summing a contiguous share of the blocks, then the shares in order.
+// The blocks' sums in order: 32 columns of a row by up to 32 rows of threads,
+// each summing a contiguous share of the blocks, then the shares in order.
 __global__ void __launch_bounds__(1024)
-db_join_kernel(const float* part, int blocks, int N, uint16_t* db, int bf16) {
+join_kernel(const float* part, int blocks, int cols, int pitch, uint16_t* out, long long ldo, int bf16) {
   __shared__ float sh[32][33];
   grid_wait();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, rows = blockDim.x >> 5;
   const int c = blockIdx.x * 32 + tx;
+  const size_t block = (size_t)gridDim.y * pitch, at = (size_t)blockIdx.y * pitch + c;
   float acc = 0.0f;
-  if (c < N) {
-    const int b0 = blocks * ty / 32, b1 = blocks * (ty + 1) / 32;
+  if (c < cols) {
+    const int shift = __ffs(rows) - 1;         // a power of two
+    const int b0 = (blocks * ty) >> shift, b1 = (blocks * (ty + 1)) >> shift;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) acc += part[(size_t)b * N + c];
+    for (int b = b0; b < b1; ++b) acc += part[b * block + at];
   }
   sh[ty][tx] = acc;
   __syncthreads();
-  if (ty == 0 && c < N) {
-#pragma unroll
-    for (int i = 1; i < 32; ++i) acc += sh[i][tx];
-    db[c] = (uint16_t)pack2(make_float2(acc, 0.0f), bf16 != 0);
+  if (ty == 0 && c < cols) {
+    acc = 0.0f;
+    for (int i = 0; i < rows; i += 4) {
+      const float v[4] = {sh[i][tx], sh[i + 1][tx], sh[i + 2][tx], sh[i + 3][tx]};
+      acc = acc + v[0] + v[1] + v[2] + v[3];
+    }
+    out[blockIdx.y * ldo + c] = (uint16_t)pack2(make_float2(acc, 0.0f), bf16 != 0);
   }
 }
 
@@ -206,8 +212,24 @@ G16Choice choose_gemm16(const G16Launch& l) {
 cudaError_t launch_gemm(G16Launch& l, cudaStream_t st) {
   l.err = op_err_address();
   if (!l.err) return cudaErrorInvalidDevice;
-  const G16Choice c = choose_gemm16(l);
-  return c.pair ? launch_gemm16_pair(l, c.bn, st) : launch_gemm16_split(l, c.bn, c.splits, st);
+  const auto launch = [&](const G16Launch& k, const G16Choice& c) {
+    return c.pair ? launch_gemm16_pair(k, c.bn, st) : launch_gemm16_split(k, c.bn, c.splits, st);
+  };
+  // Two launches where the two gradients want different forms (16 x 64 to
+  // 12288: 16.5 us, 52 in one launch; 16 x 1152 to 4608: 23, 28) and the model
+  // puts their sum a tenth lower: one launch fills the GPU better and saves the
+  // second start (16 x 512 to 512: 6.9 us, 10.6 in two launches).
+  const G16Choice both = choose_gemm16(l);
+  if (l.A[0].p && l.A[1].p) {
+    G16Launch one[2] = {l, l};
+    one[0].A[1].p = one[1].A[0].p = nullptr;
+    const G16Choice c[2] = {choose_gemm16(one[0]), choose_gemm16(one[1])};
+    if (c[0].us + c[1].us < 0.9 * both.us) {
+      const cudaError_t e = launch(one[0], c[0]);
+      return e != cudaSuccess ? e : launch(one[1], c[1]);
+    }
+  }
+  return launch(l, both);
 }
 
 // Workspace of the backward call: dP, then the column sums' partials.
@@ -215,13 +237,17 @@ struct BwdLayout {
   size_t dp, part, total;
   long long lddp;
 };
-BwdLayout bwd_layout(int M, int N, int epilogue) {
+BwdLayout bwd_layout(int M, int K, int N, int epilogue) {
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
   BwdLayout L{};
   L.lddp = ((long long)N + 7) / 8 * 8;
   L.dp = 0;
   L.part = epilogue == SVDQ_EPI_NONE ? 0 : up((size_t)M * L.lddp * 2);
   L.total = L.part + up((size_t)dp_row_blocks(M, N) * N * sizeof(float));
+  if (M <= THIN_BWD_ROWS) {             // all of it is then for the sums of dX
+    const size_t thin = up(thin16_bwd_workspace(M, K, N));
+    if (thin > L.total) L.total = thin;
+  }
   return L;
 }
 
@@ -237,6 +263,15 @@ bool ok_call(int dtype, int epilogue) {
 }
 
 }  // namespace
+
+cudaError_t launch_join(const float* part, int blocks, int rows, int cols, int pitch, uint16_t* out,
+                        long long ldo, int bf16, cudaStream_t st) {
+  const dim3 grid((unsigned)(((long long)cols + 31) / 32), (unsigned)rows);
+  int ty = 4;                 // rows of threads: no more than there are blocks to sum
+  while (ty < 32 && ty < blocks) ty *= 2;
+  return launch_op(join_kernel, grid, 32 * ty, 0, 1, st, part, blocks, cols, pitch, out, ldo, bf16);
+}
+
 }  // namespace svdq
 
 using svdq::rows_aligned16;
@@ -278,7 +313,7 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
 
 size_t svdq_linear16_backward_workspace(int M, int K, int N, int epilogue) {
   if (M <= 0 || K < 1 || N < 1 || !svdq::ok_call(SVDQ_DTYPE_BF16, epilogue)) return 0;
-  return svdq::bwd_layout(M, N, epilogue).total;
+  return svdq::bwd_layout(M, K, N, epilogue).total;
 }
 
 svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* dY, int lddy,
@@ -301,15 +336,21 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
     return SVDQ_OK;
   }
   if (!dX && !dW && !db) return SVDQ_OK;
-  if (!dY || (dW && !X) || (dX && !W) || (act && !P) || ((act || db) && !workspace))
-    return SVDQ_ERR_INVALID_ARG;
+  const bool thin = M <= svdq::THIN_BWD_ROWS && (dX || dW);
+  const bool needs_ws = act || db || (thin && dX);
+  if (!dY || (dW && !X) || (dX && !W) || (act && !P) || (needs_ws && !workspace)) return SVDQ_ERR_INVALID_ARG;
   if (!rows_aligned16(dY, lddy, 2) || (dW && !rows_aligned16(X, ldx, 2)) ||
       (dX && (!rows_aligned16(W, ldw, 2) || !rows_aligned16(dX, lddx, 2))) ||
       (act && !rows_aligned16(P, ldp, 2)) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return SVDQ_ERR_ALIGNMENT;
-  const svdq::BwdLayout L = svdq::bwd_layout(M, N, epilogue);
-  if ((act || db) && workspace_bytes < L.total) return SVDQ_ERR_SHAPE;
+  const svdq::BwdLayout L = svdq::bwd_layout(M, K, N, epilogue);
+  if (needs_ws && workspace_bytes < L.total) return SVDQ_ERR_SHAPE;
   const int bf16 = dtype == SVDQ_DTYPE_BF16;
+  if (thin) {
+    const svdq::ThinBwdCall c{dY, act ? P : nullptr, dW ? X : nullptr, dX ? W : nullptr, dX, dW, db, workspace,
+                              lddy, ldp, ldx, ldw, lddx, lddw, M, K, N, epilogue, bf16};
+    return svdq::launch_thin16_bwd(c, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  }
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const void* dP = dY;
   long long lddp = lddy;
@@ -338,9 +379,8 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
                   : epilogue == SVDQ_EPI_SILU ? svdq::dp_kernel<SVDQ_EPI_SILU>
                                               : svdq::dp_kernel<SVDQ_EPI_NONE>;
     if (svdq::launch_op(kernel, grid, 256, 0, 1, stream, d) != cudaSuccess) return SVDQ_ERR_CUDA;
-    if (d.part && svdq::launch_op(svdq::db_join_kernel, dim3((unsigned)(((long long)N + 31) / 32)), 1024, 0,
-                              1, stream, d.part, blocks, N, static_cast<uint16_t*>(db),
-                              bf16) != cudaSuccess)
+    if (d.part && svdq::launch_join(d.part, blocks, 1, N, N, static_cast<uint16_t*>(db), 0, bf16,
+                                    stream) != cudaSuccess)
       return SVDQ_ERR_CUDA;
   }
   svdq::G16Launch l{};
