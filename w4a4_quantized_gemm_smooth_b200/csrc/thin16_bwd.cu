@@ -1,6 +1,6 @@
 // Gradients of the 16-bit linear layer for up to 8 rows (the conditioning
-// vectors of modulation layers, small batches): with dP = dY epi'(P) rounded
-// to 16 bits,
+// vectors of modulation layers, small batches): with dP = dY epi'(P), in fp32
+// here, since no product takes 16-bit operands,
 //   dX [M][K] = dP W,   dW [N][K] = dP^T X,   db [N] = sum_m dP.
 //
 // Both products walk the same N x K places, one reading W, the other writing
@@ -176,7 +176,6 @@ thin16_bwd_kernel(const ThinBwdArgs a) {
         if (m >= a.M) d.x = 0.0f;
         if (m + 1 >= a.M) d.y = 0.0f;
         sum = sum + d.x + d.y;
-        d = unpack2(pack2(d, BF16), BF16);
         grad[threadIdx.x][m] = make_float2(d.x, d.x);
         grad[threadIdx.x][m + 1] = make_float2(d.y, d.y);
       }
