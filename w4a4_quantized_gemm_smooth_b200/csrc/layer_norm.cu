@@ -1,9 +1,8 @@
 // Layer norm with a scale and a shift per group of rows, and its gradients.
 //
 // A row belongs to one team (a quarter of a warp for the shortest rows, a
-// warp, or a block of 128 or 512 threads for long ones), and a team walks over
-// rows of one group, two or four at a time.  Each
-// thread copies its own 16-byte vectors of the next rows to its own places in
+// warp, or a block of 128, 256 or 512 threads for long ones), and a team walks
+// over rows of one group, one to four at a time.  Each thread copies its own 16-byte vectors of the next rows to its own places in
 // shared memory (cp.async, no barrier), so that the bytes in flight do not
 // depend on the registers that a row needs; the group's scale (with its
 // offset) and shift wait there too, in fp32, converted once per block.
@@ -66,26 +65,30 @@ __device__ __forceinline__ RowSpan block_span(int M, int rows_per_group, int spl
 // How a row of up to G NV V elements (V = 16 / sizeof(T)) is held: threads of
 // a block, teams of a block and of a warp, rows at a time and in flight per
 // team, blocks per SM, and whether the scale and shift are kept in shared
-// memory (not for the longest rows, which need the room; they are read from
-// the caches).
+// memory (wherever they fit; else every row reads them from the caches, with
+// which 1500 x 12288 took 25.4 us instead of 18.9).
+// Rows at a time: four of one vector a thread (60000 x 256: 16.1 us, 19.5 with
+// two); in blocks of 256 threads two of three vectors (2250 x 5400: 11.8 us,
+// 13.2 with one) and one of more (2250 x 7562: 16.4, 20.0 with two).
 template <typename T, int G, int NV>
 struct NormCfg {
   static constexpr int V = 16 / (int)sizeof(T), H = V / 2;
   static constexpr int THREADS = G > 128 ? G : 128;
   static constexpr int TEAMS = THREADS / G;
   static constexpr int TW = G < 32 ? 32 / G : 1;
-  static constexpr bool PSMEM = G < 512;
-  static constexpr int RF = NV == 1 ? 4 : G < 512 ? 2 : 1;     // rows at a time, forward
+  static constexpr int RF = NV == 1 ? 4 : G < 256 || (G == 256 && NV == 3) ? 2 : 1;   // rows at a time, forward
   static constexpr int DF = 2;                                 // and steps in flight
-  static constexpr int RB = RF;                                // backward (x and dy): rows at a time
+  static constexpr int RB = NV == 1 ? 4 : G < 512 ? 2 : 1;     // backward (x and dy): rows at a time
   static constexpr int DB = NV < 8 ? 2 : 1;                    // and steps in flight
-  static constexpr int SM_F = NV == 1 ? 6 : G < 512 ? 4 : 1;   // blocks per SM
-  static constexpr int SM_B = NV == 1 ? 4 : G < 512 ? 2 : 1;
-  static constexpr size_t PARAM = PSMEM ? (size_t)NV * G * V * 4 : 0;   // one fp32 row
+  static constexpr int SM_F = NV == 1 ? 6 : G < 256 ? 4 : G == 256 ? 2 : 1;    // blocks per SM
+  static constexpr int SM_B = NV == 1 ? 4 : G < 256 ? 2 : 1;
+  static constexpr size_t ROW = (size_t)NV * G * V * 4;        // one fp32 parameter row
   static constexpr size_t RING_FWD = (size_t)DF * RF * NV * THREADS * 16;
   static constexpr size_t RING_BWD = (size_t)DB * RB * 2 * NV * THREADS * 16;
-  static constexpr size_t FWD_SMEM = RING_FWD + 2 * PARAM;
-  static constexpr size_t BWD_SMEM = RING_BWD + PARAM;
+  static constexpr bool PSMEM_F = RING_FWD + 2 * ROW <= 227 * 1024;
+  static constexpr bool PSMEM_B = RING_BWD + ROW <= 227 * 1024;
+  static constexpr size_t FWD_SMEM = RING_FWD + (PSMEM_F ? 2 * ROW : 0);
+  static constexpr size_t BWD_SMEM = RING_BWD + (PSMEM_B ? ROW : 0);
   static_assert(FWD_SMEM <= 227 * 1024 && BWD_SMEM <= 227 * 1024, "shared memory");
   static_assert(TEAMS == 1 || (size_t)2 * NV * THREADS * V * 4 <= RING_BWD, "the teams' sums fit the ring");
 };
@@ -246,13 +249,13 @@ norm_kernel(const NormArgs p) {
   const uint4* ring = smem + threadIdx.x;              // vector (slot, row, i) at ((slot R + row) NV + i) TH
   const uint32_t ring_u = smem_u32(ring);
   float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_FWD);
-  float4* pb = pw + C::PARAM / 16;
+  float4* pb = pw + C::ROW / 16;
   const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
   const PT* b = p.b ? static_cast<const PT*>(p.b) + span.g * p.ldb : nullptr;
   const RowShare<T, G, NV> share(lane, p.K);
   // the parameters' loads leave first, the rows' copies next to them
-  ParamStage<PT, V, G, C::PSMEM ? NV : 1, TH> sw, sb;
-  if constexpr (C::PSMEM) {
+  ParamStage<PT, V, G, C::PSMEM_F ? NV : 1, TH> sw, sb;
+  if constexpr (C::PSMEM_F) {
     if (w) sw.load(w, p.K);
     if (b) sb.load(b, p.K);
   }
@@ -265,7 +268,7 @@ norm_kernel(const NormArgs p) {
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(span.r0 + (team + d * C::TEAMS) * R, d);
-  if constexpr (C::PSMEM) {
+  if constexpr (C::PSMEM_F) {
     if (w) sw.store(pw, p.w0);
     if (b) sb.store(pb, 0.0f);
     __syncthreads();
@@ -342,8 +345,8 @@ norm_kernel(const NormArgs p) {
       const int c = (lane + i * G) * V;
       if (i + 1 < NV || c < p.K) {
         float2 fw[H], fb[H];
-        if (w) read_param<PT, V, G, C::PSMEM>(fw, pw, w, p.K, lane, i, p.w0);
-        if (b) read_param<PT, V, G, C::PSMEM>(fb, pb, b, p.K, lane, i, 0.0f);
+        if (w) read_param<PT, V, G, C::PSMEM_F>(fw, pw, w, p.K, lane, i, p.w0);
+        if (b) read_param<PT, V, G, C::PSMEM_F>(fb, pb, b, p.K, lane, i, 0.0f);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
           const float2 r2 = splat2(rstd[k]);
@@ -398,8 +401,8 @@ norm_bwd_kernel(const NormBwdArgs p) {
   float4* pw = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(smem) + C::RING_BWD);
   const PT* w = p.w ? static_cast<const PT*>(p.w) + span.g * p.ldw : nullptr;
   const RowShare<T, G, NV> share(lane, p.K);
-  ParamStage<PT, V, G, C::PSMEM ? NV : 1, TH> sw;
-  if constexpr (C::PSMEM)
+  ParamStage<PT, V, G, C::PSMEM_B ? NV : 1, TH> sw;
+  if constexpr (C::PSMEM_B)
     if (w) sw.load(w, p.K);
   float nmu[D][R], nrs[D][R];                // the statistics of the rows in flight
   const int behind = (team % C::TW) * R;     // as in the forward kernel
@@ -438,7 +441,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
 #pragma unroll
       for (int j = 0; j < H; ++j) aw[i][j] = ab[i][j] = make_float2(0.0f, 0.0f);
   }
-  if constexpr (C::PSMEM) {
+  if constexpr (C::PSMEM_B) {
     if (w) sw.store(pw, p.w0);
     __syncthreads();
   }
@@ -468,7 +471,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 f[H];
-      if (w) read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
+      if (w) read_param<PT, V, G, C::PSMEM_B>(f, pw, w, p.K, lane, i, p.w0);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         const RowVec<T, V> xr = read_vec<T, V>(q + (2 * k * NV + i) * TH, TH);
@@ -510,7 +513,7 @@ norm_bwd_kernel(const NormBwdArgs p) {
         const int c = (lane + i * G) * V;
         if (i + 1 < NV || c < p.K) {
           float2 f[H];
-          if (w) read_param<PT, V, G, C::PSMEM>(f, pw, w, p.K, lane, i, p.w0);
+          if (w) read_param<PT, V, G, C::PSMEM_B>(f, pw, w, p.K, lane, i, p.w0);
 #pragma unroll
           for (int k = 0; k < R; ++k) {
             const RowVec<T, V> xr = read_vec<T, V>(q + (2 * k * NV + i) * TH, TH);
@@ -683,15 +686,20 @@ cudaError_t fwd_launch(NormArgs a, cudaStream_t st) {
   const cudaError_t e = allow_smem(norm_kernel<T, PT, G, NV>, C::FWD_SMEM, done);
   if (e != cudaSuccess) return e;
   const long long groups = ((long long)a.M + a.rows_per_group - 1) / a.rows_per_group;
-  a.splits = split_rows(a.M, a.rows_per_group, G == 512 ? 2 : C::SM_F, C::TEAMS);
+  a.splits = split_rows(a.M, a.rows_per_group, C::PSMEM_F ? C::SM_F : 2, C::TEAMS);
   return launch_op(norm_kernel<T, PT, G, NV>, dim3((unsigned)(groups * a.splits)), C::THREADS,
                    C::FWD_SMEM, 1, st, a);
 }
 
 // Team and vectors per thread for a row of `vecs` 16-byte vectors of V
 // elements (SVDQ_NORM_MAX_K elements at most): the fewest that hold the row,
-// so that only a thread's last vector can lie past it.
-template <int V, typename F>
+// so that only a thread's last vector can lie past it.  A warp per row while
+// it fits (16384 x 1152: 14.3 us, 21.3 with 128 threads), 256 threads rather
+// than 512 (2250 x 7562: 16.4, 28.3), which forward are also better than 128
+// with five vectors (2250 x 4608: 10.8, 14.0) and backward are not (a block of
+// 256 has the SM for itself: 2250 x 5400 27 us, 2250 x 4608 19.6 with two of
+// 128).
+template <int V, bool FWD, typename F>
 cudaError_t dispatch_row(int vecs, F&& f) {
   if (vecs <= 8 * 1) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
   if (vecs <= 16 * 1) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
@@ -703,8 +711,11 @@ cudaError_t dispatch_row(int vecs, F&& f) {
   if (vecs <= 128 * 2) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
   if (vecs <= 128 * 3) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 3>());
   if (vecs <= 128 * 4) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 4>());
-  if (vecs <= 128 * 5) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 5>());
-  if (vecs <= 512 * 2) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+  if constexpr (!FWD)
+    if (vecs <= 128 * 5) return f(std::integral_constant<int, 128>(), std::integral_constant<int, 5>());
+  if (vecs <= 256 * 3) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 3>());
+  if (vecs <= 256 * 4) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
+  if (vecs <= 256 * 5) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 5>());
   if (vecs <= 512 * 3) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 3>());
   if constexpr (V == 4) {
     if (vecs <= 512 * 4) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
@@ -719,7 +730,7 @@ cudaError_t dispatch_row(int vecs, F&& f) {
 template <typename T, typename PT>
 cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
-  return dispatch_row<V>((a.K + V - 1) / V, [&](auto g, auto nv) {
+  return dispatch_row<V, true>((a.K + V - 1) / V, [&](auto g, auto nv) {
     return fwd_launch<T, PT, decltype(g)::value, decltype(nv)::value>(a, st);
   });
 }
@@ -745,7 +756,7 @@ template <typename T, typename PT>
 cudaError_t bwd(const NormBwdArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
   const long long groups = ((long long)a.M + a.rows_per_group - 1) / a.rows_per_group;
-  cudaError_t e = dispatch_row<V>((a.K + V - 1) / V, [&](auto g, auto nv) {
+  cudaError_t e = dispatch_row<V, false>((a.K + V - 1) / V, [&](auto g, auto nv) {
     return bwd_launch<T, PT, decltype(g)::value, decltype(nv)::value>(a, groups, st);
   });
   if (e != cudaSuccess || a.splits == 1 || (!a.dw && !a.db)) return e;
