@@ -433,6 +433,15 @@ def test_norm_groups(M, K, groups, off):
     check_norm(M, K, F32, F32, groups, off, seed=K)
 
 
+@pytest.mark.parametrize("M,K,groups", [(1500, 5130, 1), (900, 2601, 3), (700, 7562, 2), (500, 10241, 1), (310, 14001, 3),
+                                        (300, 16384, 1)])
+@pytest.mark.parametrize("dtype,pt", [(BF16, BF16), (F16, F32), (F32, F32)])
+def test_norm_many_long_rows(M, K, groups, dtype, pt):
+    """More rows than blocks, of the lengths at which whole blocks work."""
+    check_norm(M, K, dtype, pt, groups, 1.0, seed=K)
+    check_norm_bwd(M, K, dtype, pt, groups, 1.0, seed=K)
+
+
 @pytest.mark.parametrize("offset", [100.0, -3000.0])
 @pytest.mark.parametrize("K", [64, 1153, 9000])
 def test_norm_large_mean(offset, K):
