@@ -187,3 +187,23 @@ def test_binding_rejects_unfit_tensors():
 def test_rope_frequencies():
     assert S.rope_frequencies([2, 4], 100.0) == pytest.approx(
         [1.0, 0.1, 1.0, 100.0 ** -0.25, 0.1, 100.0 ** -0.75], rel=1e-15)
+
+
+def test_programmatic_kernels_load_coherently():
+    """Kernels that are resident while the one before them still writes (they
+    call grid_wait) make no non-coherent load, nor let the compiler choose one
+    through __restrict__."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(S.__file__), "csrc")
+    shared = ("elem.cuh", "gemm16.cuh")
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        if "grid_wait()" not in text and os.path.basename(path) not in shared:
+            continue
+        seen += 1
+        found = re.findall(r"__ldg\b|__restrict__|\bld\.global\S*\.nc\b", text)
+        assert not found, f"{os.path.basename(path)}: {found}"
+    assert seen >= 8

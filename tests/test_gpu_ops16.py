@@ -853,6 +853,46 @@ def test_chains_keep_their_order():
         assert torch.equal(chain(False), want)
 
 
+@pytest.mark.parametrize("M", [1, 8, 16])
+@pytest.mark.parametrize("captured", [False, True])
+def test_few_row_products_in_a_row(M, captured):
+    """Products of few rows that follow one another with nothing in between:
+    each reads the rows and the bias that the one before has just written, and
+    adds in place."""
+    g = gen(M)
+    K = 264
+    X0, W0 = rows(g, M, K, BF16), rows(g, K, K, BF16, K ** -0.5)
+
+    def chain(sync):
+        X, Y, W = X0.clone(), torch.zeros((M, K), dtype=BF16, device="cuda"), W0.clone()
+        b = torch.zeros((1, K), dtype=BF16, device="cuda")
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+
+        def run():
+            for _ in range(6):
+                S.svdq_linear16(X, W, Y, residual=Y)                      # Y += X W^T
+                wait()
+                S.svdq_linear16(Y, W, X, bias=b[0], residual=X, epilogue=S.EPI_SILU)
+                wait()
+                S.svdq_linear16(X[:1], W, b, epilogue=S.EPI_SILU)         # the next bias
+                wait()
+        if captured and not sync:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+            graph.replay()
+        else:
+            run()
+        torch.cuda.synchronize()
+        return X, Y, b
+
+    want = chain(True)
+    assert all(bool(t.isfinite().all()) for t in want)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+
+
 FIRST_CAPTURED = """
 import sys, torch
 sys.path.insert(0, {root!r})

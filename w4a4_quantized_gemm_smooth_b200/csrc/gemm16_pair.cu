@@ -240,7 +240,7 @@ gemm16_pair_kernel(const __grid_constant__ G16Problem p0, const __grid_constant_
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = n0 + 32 * c + lane;
-        bias[c] = p.bias && col < p.N ? unpack2(__ldg(p.bias + col), p.bf16 != 0).x : 0.0f;
+        bias[c] = p.bias && col < p.N ? unpack2(p.bias[col], p.bf16 != 0).x : 0.0f;
       }
       if (lane == 0) {
         tma_store_wait_read0();                       // the previous tile's boxes have left

@@ -174,7 +174,7 @@ gemm16_split_kernel(const __grid_constant__ G16Problem p0, const __grid_constant
 #pragma unroll
       for (int c = 0; c < L::CH; ++c) {
         const int col = n0 + 32 * (c0 + c) + lane;
-        bias_s[32 * c + lane] = p.bias && col < p.N ? unpack2(__ldg(p.bias + col), p.bf16 != 0).x : 0.0f;
+        bias_s[32 * c + lane] = p.bias && col < p.N ? unpack2(p.bias[col], p.bf16 != 0).x : 0.0f;
       }
       __syncwarp();
     }

@@ -25,7 +25,9 @@ inline bool rows_aligned16(const void* p, int ld, int esize) {
 // it in the stream runs out (its blocks then set up their shared memory and
 // wait), which hides the launch behind that kernel's last blocks.  Every such
 // kernel calls grid_wait() in all its threads before it touches global
-// memory, so that what it reads and overwrites is in order.
+// memory, so that what it reads and overwrites is in order.  It reads with
+// plain loads or copies: a non-coherent load (ld.global.nc) wants memory that
+// nothing writes while the kernel is resident, and the kernel before it does.
 template <typename... P, typename... A>
 cudaError_t launch_op(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
                       cudaStream_t st, A&&... args) {

@@ -80,9 +80,9 @@ thin16_kernel(const ThinArgs a) {
     for (int u = 0; u < U; ++u) {
       const int k = 32 * (r0 + u);
       if (r0 + u < end) {
-        wq[u] = __ldg(reinterpret_cast<const uint4*>(w + k));
+        wq[u] = *reinterpret_cast<const uint4*>(w + k);
 #pragma unroll
-        for (int j = 0; j < XT; ++j) xq[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + k));
+        for (int j = 0; j < XT; ++j) xq[u][j] = *reinterpret_cast<const uint4*>(x[j] + k);
       }
     }
 #pragma unroll
