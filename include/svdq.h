@@ -524,8 +524,10 @@ svdq_status svdq_linear_nvfp4(const svdq_weights* w, int M, const uint8_t* xq,
  *     else SVDQ_ERR_ALIGNMENT, while row lengths (K, N) may be any size: the
  *     elements between a row's length and its leading dimension are neither
  *     read nor written;
- *   - the arrays are on the current device; outputs overlap no input and no
- *     other output except where stated;
+ *   - the arrays are on the current device; outputs (and a workspace) overlap
+ *     no input and no other output except where stated, else
+ *     SVDQ_ERR_INVALID_ARG.  Slices of one buffer whose rows interleave do not
+ *     overlap;
  *   - calls are asynchronous on `stream`, allocate nothing and may be
  *     captured into a graph; a kernel may be brought up while the one before
  *     it on the stream runs out, and touches memory once that has finished;

@@ -163,6 +163,66 @@ def test_rope_refusals():
     S.lib().svdq_rope_free(h)
 
 
+# an output that shares memory with another array of its call: blocks run in any
+# order, so the result would depend on timing
+def test_linear16_refuses_overlap():
+    M, K, N = 8, 64, 32
+    x, w, y = M * K * 2, N * K * 2, M * N * 2
+    assert linear(Y=A) == INVALID and linear(Y=B) == INVALID             # Y is X, Y is W
+    assert linear(Y=A + x - 16) == INVALID and linear(Y=B + w - 16) == INVALID and linear(Y=A - y + 16) == INVALID
+    assert linear(bias=C) == INVALID and linear(bias=C + y - 16) == INVALID
+    assert linear(R=C + 16, ldr=32) == INVALID and linear(R=C - 64, ldr=32) == INVALID   # not quite in place
+    assert linear(P=C + y - 64, ldp=32) == INVALID
+    for P in (A, B, A + x - 16):
+        assert linear(P=P, ldp=32) == INVALID
+    assert linear(P=D, ldp=32, R=D + y - 16, ldr=32) == INVALID
+    assert linear(P=D, ldp=32, bias=D + 16) == INVALID
+    assert linear(R=C, ldr=32, P=C + 16, ldp=32) == INVALID              # in place, the pre-activation over it
+    assert linear(M=200, ldx=128, ldy=128, Y=A + 96) == INVALID          # columns 48 to 79 of X's rows of 64 in 128
+    assert linear(M=20, Y=A) == INVALID and linear(M=3000, Y=A) == INVALID
+
+
+def test_linear16_backward_refuses_overlap():
+    for name, others in (("dX", "dY X W P"), ("dW", "dY X W P dX"), ("db", "dY X W P dX dW"), ("ws", "dY X W P dX dW db")):
+        for other in others.split():
+            at = dict(dY=A, X=B, W=C, P=D, dX=E, dW=F, db=G)[other]
+            assert linear_bwd(**{name: at}) == INVALID, (name, other)
+            assert linear_bwd(M=40, **{name: at}) == INVALID, (name, other)
+    assert linear_bwd(dX=B + 8 * 64 * 2 - 16) == INVALID                 # the last bytes of X
+
+
+def test_layer_norm_refuses_overlap():
+    assert norm(Y=A + 16) == INVALID and norm(Y=A + 4 * 64 * 2 - 16) == INVALID
+    assert norm(Y=B) == INVALID and norm(Y=C) == INVALID
+    for k in ("mean", "rstd"):
+        for at in (A, B, C, D, D + 4 * 64 * 2 - 4):
+            assert norm(**{k: at}) == INVALID
+    assert norm(mean=E, rstd=E) == INVALID and norm(mean=E, rstd=E + 12) == INVALID
+    H = 0x10000000           # apart from the others: 4096 rows of 64 take 512 KB
+    far = dict(dY=H, X=2 * H, mean=3 * H, rstd=4 * H, w=5 * H, dX=6 * H, dw=7 * H, db=8 * H, ws=9 * H)
+    for name, others in (("dX", "mean rstd w"), ("dw", "dY X mean rstd w dX"), ("db", "dY X mean rstd w dX dw"),
+                         ("ws", "dY X mean rstd w dX dw db")):
+        for other in others.split():
+            assert norm_bwd(**{**far, name: far[other]}) == INVALID, (name, other)
+    assert norm_bwd(**{**far, "dX": H + 128}) == INVALID and norm_bwd(**{**far, "dX": 2 * H - 128}) == INVALID
+
+
+def test_rope_refuses_overlap():
+    _, h = plan()
+
+    def rope(T=4, H=2, D=128, pos=A, rows=4, X=B, xt=256, xh=128, Y=C, yt=256, yh=128):
+        return S.lib().svdq_rope(h, 0, T, H, D, pos, rows, 3, X, xt, xh, Y, yt, yh, 0, None)
+
+    size = 4 * 256 * 2
+    assert rope(Y=B + 2) == INVALID and rope(Y=B - size + 2) == INVALID and rope(Y=B + size - 2) == INVALID
+    assert rope(Y=B + 256) == INVALID                                    # head 0 over head 1
+    assert rope(Y=B + 512, xt=512, yt=512, yh=128, T=3, H=3) == INVALID  # rows of 512: the third head meets the next
+    assert rope(xt=0, Y=B + 256) == INVALID and rope(xh=0, Y=B + 512) == INVALID    # broadcast inputs
+    assert rope(xt=128, xh=512, Y=B) == INVALID                          # other strides, the same memory
+    assert rope(Y=A - 256) == INVALID and rope(pos=C + size - 4) == INVALID
+    S.lib().svdq_rope_free(h)
+
+
 def test_binding_rejects_unfit_tensors():
     x = torch.zeros((4, 8), dtype=torch.bfloat16)
     w = torch.zeros((16, 8), dtype=torch.bfloat16)

@@ -960,6 +960,42 @@ def test_two_graphs_on_forked_streams():
         assert torch.equal(Z, want) and torch.equal(N, wantn) and torch.equal(Y, want + want)
 
 
+def test_slices_of_one_buffer_are_no_overlap():
+    """Inputs and outputs that interleave in one buffer are taken, and give
+    what separate arrays give; an output over an input is refused."""
+    g = gen(61)
+    M, K, N = 70, 64, 48
+    W = rows(g, N, K, BF16, 0.1)
+    buf = torch.full((M, 512), 77.0, dtype=BF16, device="cuda")
+    X, Y, P, R, dY, dX, Nm = buf[:, :64], buf[:, 64:112], buf[:, 112:160], buf[:, 160:208], buf[:, 208:256], \
+        buf[:, 256:320], buf[:, 320:384]
+    for t in (X, R, dY):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    y, p, dx, nm = (torch.empty((M, n), dtype=BF16, device="cuda") for n in (N, N, K, K))
+    S.svdq_linear16(X, W, Y, residual=R, epilogue=S.EPI_GELU, preact=P)
+    S.svdq_linear16(X.contiguous(), W, y, residual=R.contiguous(), epilogue=S.EPI_GELU, preact=p)
+    ws = torch.empty((S.svdq_linear16_backward_workspace(M, K, N, S.EPI_GELU),), dtype=torch.uint8, device="cuda")
+    S.svdq_linear16_backward(dY, X, W, P, dX, None, None, ws, S.EPI_GELU)
+    S.svdq_linear16_backward(dY.contiguous(), X, W, p, dx, None, None, ws, S.EPI_GELU)
+    S.svdq_layer_norm(X, Nm)
+    S.svdq_layer_norm(X.contiguous(), nm)
+    plan = S.svdq_rope_create([4], S.rope_frequencies([4]))
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")[:, None]
+    qk = torch.empty((M, 4, 16), dtype=BF16, device="cuda")
+    S.svdq_rope(plan, pos, X.unflatten(1, (4, 16)), buf[:, 384:448].unflatten(1, (4, 16)))
+    S.svdq_rope(plan, pos, X.unflatten(1, (4, 16)).contiguous(), qk)
+    # the input's heads are shared (a stride of 0), its rows interleave with the output's
+    S.svdq_rope(plan, pos, buf[:, None, :16].expand(M, 4, 16), buf[:, 448:512].unflatten(1, (4, 16)))
+    assert torch.equal(Y, y) and torch.equal(P, p) and torch.equal(dX, dx) and torch.equal(Nm, nm)
+    assert torch.equal(buf[:, 384:448], qk.flatten(1)) and torch.equal(buf[:, 448:512].unflatten(1, (4, 16))[:, 3], qk[:, 0])
+    for call in (lambda: S.svdq_linear16(X, W, buf[:, 32:80]), lambda: S.svdq_linear16(X, W, X[:, :N]),
+                 lambda: S.svdq_layer_norm(X, buf[:, 56:120]), lambda: S.svdq_layer_norm(X[1:], X[:-1]),
+                 lambda: S.svdq_linear16(W, W, W[:, :48])):
+        with pytest.raises(S.SVDQError) as e:
+            call()
+        assert e.value.status == 1
+
+
 # ------------------------------------------- the paths of the quantised layers
 def _packed(K, N, rank, seed):
     import synth

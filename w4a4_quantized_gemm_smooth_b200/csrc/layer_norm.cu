@@ -806,6 +806,17 @@ svdq_status svdq_layer_norm(int dtype, int param_dtype, int M, int K, const void
       (weight && !rows_aligned16(weight, ldw, ps)) || (bias && !rows_aligned16(bias, ldb, ps)) ||
       (reinterpret_cast<uintptr_t>(mean) & 3) || (reinterpret_cast<uintptr_t>(rstd) & 3))
     return SVDQ_ERR_ALIGNMENT;
+  {
+    using svdq::extent_flat;
+    using svdq::extent_rows;
+    const long long groups = rows_per_group ? ((long long)M + rows_per_group - 1) / rows_per_group : 1;
+    const svdq::Extent x = extent_rows(X, M, K, ldx, es), y = extent_rows(Y, M, K, ldy, es),
+                       w = extent_rows(weight, groups, K, ldw, ps), b = extent_rows(bias, groups, K, ldb, ps),
+                       mu = extent_flat(mean, 4ll * M), rs = extent_flat(rstd, 4ll * M);
+    if ((Y != X && svdq::overlap(y, x)) || svdq::overlaps_any(y, {w, b, mu, rs}) ||
+        svdq::overlaps_any(mu, {x, w, b, rs}) || svdq::overlaps_any(rs, {x, w, b}))
+      return SVDQ_ERR_INVALID_ARG;
+  }
   svdq::NormArgs a{};
   a.x = X; a.w = weight; a.b = bias; a.y = Y; a.mean = mean; a.rstd = rstd;
   a.ldx = ldx; a.ldw = ldw; a.ldb = ldb; a.ldy = ldy;
@@ -863,6 +874,20 @@ svdq_status svdq_layer_norm_backward(int dtype, int param_dtype, int M, int K, c
     if (!workspace) return SVDQ_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return SVDQ_ERR_ALIGNMENT;
     if (workspace_bytes < need) return SVDQ_ERR_SHAPE;
+  }
+  {
+    using svdq::extent_flat;
+    using svdq::extent_rows;
+    const long long groups = ((long long)M + a.rows_per_group - 1) / a.rows_per_group;
+    const svdq::Extent dy = extent_rows(dY, M, K, lddy, es), x = extent_rows(X, M, K, ldx, es),
+                       w = extent_rows(weight, groups, K, ldw, ps), mu = extent_flat(mean, 4ll * M),
+                       rs = extent_flat(rstd, 4ll * M), gx = extent_rows(dX, M, K, lddx, es),
+                       gw = extent_rows(dweight, groups, K, lddw, ps), gb = extent_rows(dbias, groups, K, lddb, ps),
+                       ws = extent_flat(need ? workspace : nullptr, (long long)need);
+    if ((dX != dY && svdq::overlap(gx, dy)) || (dX != X && svdq::overlap(gx, x)) ||
+        svdq::overlaps_any(gx, {w, mu, rs, gw, gb, ws}) || svdq::overlaps_any(gw, {dy, x, w, mu, rs, gb, ws}) ||
+        svdq::overlaps_any(gb, {dy, x, w, mu, rs, ws}) || svdq::overlaps_any(ws, {dy, x, w, mu, rs}))
+      return SVDQ_ERR_INVALID_ARG;
   }
   a.dy = dY; a.x = X; a.mean = mean; a.rstd = rstd; a.w = weight;
   a.dx = dX; a.dw = dweight; a.db = dbias; a.part = static_cast<float*>(workspace);

@@ -291,6 +291,15 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
       (bias && !svdq::is_aligned16(bias)) || (R && !rows_aligned16(R, ldr, 2)) ||
       (P && !rows_aligned16(P, ldp, 2)))
     return SVDQ_ERR_ALIGNMENT;
+  {
+    using svdq::extent_rows;
+    const bool in_place = R == Y;
+    const svdq::Extent x = extent_rows(X, M, K, ldx, 2), w = extent_rows(W, N, K, ldw, 2),
+                       b = svdq::extent_flat(bias, 2ll * N), r = extent_rows(R, M, N, ldr, 2),
+                       y = extent_rows(Y, M, N, ldy, 2), p = extent_rows(P, M, N, ldp, 2);
+    if (svdq::overlaps_any(y, {x, w, b, in_place ? p : r, p}) || svdq::overlaps_any(p, {x, w, b, r}))
+      return SVDQ_ERR_INVALID_ARG;
+  }
   svdq::G16Launch l{};
   l.kind = svdq::G16Kind::Forward;
   l.bf16 = dtype == SVDQ_DTYPE_BF16;
@@ -345,6 +354,18 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
     return SVDQ_ERR_ALIGNMENT;
   const svdq::BwdLayout L = svdq::bwd_layout(M, K, N, epilogue);
   if (needs_ws && workspace_bytes < L.total) return SVDQ_ERR_SHAPE;
+  {
+    using svdq::extent_rows;
+    const svdq::Extent dy = extent_rows(dY, M, N, lddy, 2), x = extent_rows(dW ? X : nullptr, M, K, ldx, 2),
+                       w = extent_rows(dX ? W : nullptr, N, K, ldw, 2),
+                       p = extent_rows(act ? P : nullptr, M, N, ldp, 2),
+                       ws = svdq::extent_flat(needs_ws ? workspace : nullptr, (long long)L.total),
+                       gx = extent_rows(dX, M, K, lddx, 2), gw = extent_rows(dW, N, K, lddw, 2),
+                       gb = svdq::extent_flat(db, 2ll * N);
+    if (svdq::overlaps_any(gx, {dy, x, w, p, ws, gw, gb}) || svdq::overlaps_any(gw, {dy, x, w, p, ws, gb}) ||
+        svdq::overlaps_any(gb, {dy, x, w, p, ws}) || svdq::overlaps_any(ws, {dy, x, w, p}))
+      return SVDQ_ERR_INVALID_ARG;
+  }
   const int bf16 = dtype == SVDQ_DTYPE_BF16;
   if (thin) {
     const svdq::ThinBwdCall c{dY, act ? P : nullptr, dW ? X : nullptr, dX ? W : nullptr, dX, dW, db, workspace,

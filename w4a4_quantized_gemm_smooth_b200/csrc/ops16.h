@@ -2,6 +2,7 @@
 // The entry points beside them validate; these only launch.
 #pragma once
 
+#include "overlap.h"
 #include "svdq_internal.h"
 
 namespace svdq {

@@ -307,6 +307,17 @@ svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int hea
   if ((reinterpret_cast<uintptr_t>(X) & e) || (reinterpret_cast<uintptr_t>(Y) & e) ||
       (reinterpret_cast<uintptr_t>(positions) & 3))
     return SVDQ_ERR_ALIGNMENT;
+  {
+    const int es = svdq::dtype_size(dtype);
+    auto extent = [&](const void* p, long long token, long long head) {
+      return svdq::extent(p, (long long)head_dim * es, tokens, heads, token * es, head * es);
+    };
+    const svdq::Extent y = extent(Y, ldy_token, ldy_head);
+    const svdq::Extent pos = svdq::extent_rows(positions, pos_rows < tokens ? pos_rows : tokens, plan->t.axes,
+                                               ld_pos, 4);
+    if ((X != Y && svdq::overlap(y, extent(X, ldx_token, ldx_head))) || svdq::overlap(y, pos))
+      return SVDQ_ERR_INVALID_ARG;
+  }
   return svdq::launch_rope(plan, dtype, tokens, heads, head_dim, positions, pos_rows, ld_pos, X,
                            ldx_token, ldx_head, Y, ldy_token, ldy_head, inverse,
                            stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
