@@ -556,6 +556,53 @@ def test_norm_backward_without_weight():
     check_norm_bwd(300, 1152, BF16, BF16, affine=False)
 
 
+@pytest.mark.parametrize("wshape,bshape", [("shared", "group"), ("group", "shared"), ("shared", "shared"),
+                                           ("row", "group"), ("group", "row"), ("shared", None), (None, "row")])
+@pytest.mark.parametrize("M,K,rpg", [(300, 1152, 77), (40, 136, 1), (2000, 4608, 500), (9, 64, 9), (9, 64, 20)])
+def test_norm_layer_sums_the_gradient_of_a_shared_parameter(M, K, rpg, wshape, bshape):
+    """A scale or a shift that all groups share has one gradient, over all rows."""
+    g = gen(M + K)
+    groups = -(-M // rpg)
+    shape = {"shared": (K,), "row": (1, K), "group": (groups, K)}
+    w, b = (None if s is None else torch.randn(shape[s], generator=g, device="cuda") for s in (wshape, bshape))
+    X, dY = rows(g, M, K, BF16), rows(g, M, K, BF16)
+    layer = S.LayerNorm(w, b, weight_offset=1.0)
+    layer.forward(X, rows_per_group=rpg, save=True)
+    dX, dw, db = layer.backward(dY)
+    u = 2.0 ** -24
+    x, dy, r = X.double(), dY.double(), layer.rstd.double()[:, None]
+    h = (x - layer.mean.double()[:, None]) * r
+    grp = torch.arange(M, device="cuda") // rpg
+    ww = 1.0 if w is None else (w.double().expand(groups, K)[grp] + 1.0)
+    t = dy * ww
+    th = t * h
+    ref = r * (t - t.mean(1, keepdim=True) - h * th.mean(1, keepdim=True))
+    e = r * (4 * u * t.abs() + 84 * u * t.abs().mean(1, keepdim=True)
+             + h.abs() * 90 * u * th.abs().mean(1, keepdim=True)
+             + 6 * u * ((h * th.mean(1, keepdim=True)).abs() + t.mean(1, keepdim=True).abs()))
+    close(dX, ref, half(BF16) * (ref.abs() + e) + e, "dX")
+    for p, got, terms in ((w, dw, dy * h), (b, db, dy)):
+        if p is None:
+            assert got is None
+            continue
+        assert got.shape == p.shape and got.dtype == p.dtype
+        n = p.shape[0] if p.dim() == 2 else 1
+        at = grp if n == groups else torch.zeros_like(grp)
+        zero = torch.zeros((n, K), dtype=torch.float64, device="cuda")
+        count = torch.bincount(at, minlength=n)[:, None]
+        ref = zero.index_add(0, at, terms)
+        e = (count + 3) * u * zero.index_add(0, at, terms.abs())
+        close(got.reshape(n, K), ref, half(F32) * (ref.abs() + e) + e, "parameter")
+
+
+def test_norm_layer_without_rows_has_zero_gradients():
+    e = torch.empty((0, 64), dtype=BF16, device="cuda")
+    layer = S.LayerNorm(torch.ones((64,), device="cuda"), torch.ones((1, 64), device="cuda"))
+    layer.forward(e, rows_per_group=4, save=True)
+    dX, dw, db = layer.backward(e)
+    assert dX.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
+
+
 @pytest.mark.parametrize("scale", [1e-18, 1e15])
 @pytest.mark.parametrize("K", [96, 1300])
 def test_norm_of_very_small_and_large_rows(scale, K):

@@ -775,7 +775,8 @@ class LayerNorm:
 
     forward(X) returns the norm on the current stream; with save=True it
     keeps X and the statistics for backward(dY), which returns
-    (dX, dweight, dbias).  Buffers are reallocated only when X's shape or
+    (dX, dweight, dbias), a parameter's gradient in the parameter's shape (one
+    that all groups share, [K] or [1, K], is summed over them).  Buffers are reallocated only when X's shape or
     type changes, and the next call reuses them.
     """
 
@@ -804,17 +805,27 @@ class LayerNorm:
             raise RuntimeError("backward needs a forward call with save=True")
         X, rpg = self._saved
         M, K = X.shape
-        key = (M, K, X.dtype, rpg)
+        w, b = self.weight, self.bias
+        key = (M, K, X.dtype, rpg, *((p.shape, p.dtype) for p in (w, b) if p is not None))
         if key != self._keyb:
-            groups = -(-M // rpg) if rpg > 0 else 1
-            n = svdq_layer_norm_backward_workspace(M, K, rpg)
+            n = max(svdq_layer_norm_backward_workspace(M, K, r) for r in (0, rpg))
             self.ws = torch.empty((n,), dtype=torch.uint8, device=X.device) if n else None
             self.dX = Linear16._empty(M, K, X)
-            grad = lambda p: None if p is None else Linear16._empty(groups, K, p)
-            self.dw, self.db = grad(self.weight), grad(self.bias)
+            rows = lambda p: Linear16._empty(p.shape[0] if p.dim() == 2 else 1, K, p)
+            grad = lambda p: None if p is None else rows(p) if p.dim() == 2 else rows(p)[0]
+            self.dw, self.db = grad(w), grad(b)
             self._keyb = key
-        svdq_layer_norm_backward(dY, X, self.mean, self.rstd, self.dX, self.weight,
-                                 self.weight_offset, rpg, self.dw, self.db, self.ws)
+        # a parameter that all groups share has one gradient, over all rows: where the
+        # other has a row per group, a second pass over the rows sums it
+        per_group = lambda p: p is not None and p.dim() == 2 and p.shape[0] != 1
+        if per_group(w) or per_group(b):
+            one = [None if per_group(p) else g for p, g in ((w, self.dw), (b, self.db))]
+            own = [g if per_group(p) else None for p, g in ((w, self.dw), (b, self.db))]
+        else:
+            rpg, one, own = 0, [None, None], [self.dw, self.db]
+        svdq_layer_norm_backward(dY, X, self.mean, self.rstd, self.dX, w, self.weight_offset, rpg, *own, self.ws)
+        if one != [None, None]:
+            svdq_layer_norm_backward(dY, X, self.mean, self.rstd, None, None, 0.0, 0, *one, self.ws)
         return self.dX, self.dw, self.db
 
     __call__ = forward
