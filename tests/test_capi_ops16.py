@@ -244,6 +244,20 @@ def test_binding_rejects_unfit_tensors():
     p.free()
 
 
+def test_norm_layer_refuses_to_save_what_it_overwrites():
+    """The check stands before the call, so it needs no GPU."""
+    x = torch.zeros((4, 8), dtype=torch.bfloat16)
+    norm = S.LayerNorm()
+    with pytest.raises(ValueError, match="save=True"):
+        norm.forward(x, out=x, save=True)
+    with pytest.raises(ValueError, match="CUDA"):       # the call itself, which wants a GPU's tensors
+        norm.forward(x, out=x)
+    with pytest.raises(ValueError, match="save=True"):  # its own buffer, fed back
+        norm.forward(norm.Y, save=True)
+    with pytest.raises(RuntimeError):
+        norm.backward(x)
+
+
 def test_rope_frequencies():
     assert S.rope_frequencies([2, 4], 100.0) == pytest.approx(
         [1.0, 0.1, 1.0, 100.0 ** -0.25, 0.1, 100.0 ** -0.75], rel=1e-15)

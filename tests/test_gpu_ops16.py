@@ -595,6 +595,20 @@ def test_norm_layer_sums_the_gradient_of_a_shared_parameter(M, K, rpg, wshape, b
         close(got.reshape(n, K), ref, half(F32) * (ref.abs() + e) + e, "parameter")
 
 
+def test_norm_layer_in_place_keeps_nothing():
+    g = gen(3)
+    X = rows(g, 50, 72, BF16)
+    layer, Y = S.LayerNorm(), out(50, 72, BF16)
+    layer.forward(X, out=Y)
+    with pytest.raises(ValueError):
+        layer.forward(X, out=X, save=True)
+    assert layer.forward(X, out=X) is X and torch.equal(X, Y)
+    with pytest.raises(RuntimeError):
+        layer.backward(X)
+    e = torch.empty((0, 72), dtype=BF16, device="cuda")
+    layer.forward(e, out=e, save=True)                  # nothing is overwritten
+
+
 def test_norm_layer_without_rows_has_zero_gradients():
     e = torch.empty((0, 64), dtype=BF16, device="cuda")
     layer = S.LayerNorm(torch.ones((64,), device="cuda"), torch.ones((1, 64), device="cuda"))

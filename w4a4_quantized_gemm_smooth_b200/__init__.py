@@ -722,8 +722,9 @@ class Linear16:
 
     forward(X) returns epi(X W^T + b) + residual on the current stream; with
     save=True it keeps X and the pre-activation for backward(dY), which
-    returns (dX, dW, db).  Buffers are reallocated only when M changes, and
-    the next call reuses them.
+    returns (dX, dW, db); X is kept by reference and has to stay as it is until
+    then.  Buffers are reallocated only when M changes, and the next call
+    reuses them.
     """
 
     def __init__(self, weight, bias=None, epilogue: int = EPI_NONE):
@@ -776,8 +777,11 @@ class LayerNorm:
     forward(X) returns the norm on the current stream; with save=True it
     keeps X and the statistics for backward(dY), which returns
     (dX, dweight, dbias), a parameter's gradient in the parameter's shape (one
-    that all groups share, [K] or [1, K], is summed over them).  Buffers are reallocated only when X's shape or
-    type changes, and the next call reuses them.
+    that all groups share, [K] or [1, K], is summed over them).  X is kept by
+    reference and has to stay as it is until then, so with save=True out cannot
+    be X (ValueError); without it the norm may run in place.  Buffers are
+    reallocated only when X's shape or type changes, and the next call reuses
+    them.
     """
 
     def __init__(self, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0):
@@ -794,6 +798,8 @@ class LayerNorm:
             self.rstd = torch.empty_like(self.mean)
             self._key = (M, K, X.dtype)
         Y = self.Y if out is None else out
+        if save and X.numel() and Y.data_ptr() == X.data_ptr():
+            raise ValueError("save=True keeps X for backward: out cannot be X itself")
         svdq_layer_norm(X, Y, self.weight, self.bias, self.eps, self.weight_offset, rows_per_group,
                         self.mean if save else None, self.rstd if save else None)
         self._saved = (X, rows_per_group) if save else None
