@@ -68,6 +68,42 @@ def test_linear16_backward_refusals():
     assert S.svdq_linear16_backward_workspace(1000, 64, 33, S.EPI_SILU) >= 1000 * 40 * 2
 
 
+def test_linear16_backward_workspace_of_each_choice():
+    """The query is enough for every choice of gradients, and a call asks for no
+    more than it uses."""
+    at = [i << 36 for i in range(1, 9)]
+    dY, X, W, P, dX, dW, ws = at[:7]
+
+    def need(M, K, N, epi, want_x, want_w):
+        """The fewest bytes with which a call for db passes its check of the
+        workspace.  db lies over dY, which is refused behind it: no launch."""
+        k, n = (-(-v // 8) * 8 for v in (K, N))
+        call = lambda size: S.lib().svdq_linear16_backward(
+            0, M, K, N, dY, n, X, k, W, k, P, n, epi, dX if want_x else None, k, dW if want_w else None, k, dY, ws,
+            size, None)
+        lo, hi = 0, 1 << 34
+        assert call(hi) == INVALID
+        while lo < hi:
+            mid = (lo + hi) // 2
+            rc = call(mid)
+            assert rc in (SHAPE, INVALID)
+            lo, hi = (mid + 1, hi) if rc == SHAPE else (lo, mid)
+        return lo
+
+    for M in (1, 3, 8, 9, 32, 33, 1000):
+        for K in (1, 64, 1152, 28672):
+            for N in (1, 300, 8192):
+                for epi in (S.EPI_NONE, S.EPI_GELU):
+                    query = S.svdq_linear16_backward_workspace(M, K, N, epi)
+                    for want in ((True, True), (True, False), (False, True), (False, False)):
+                        n = need(M, K, N, epi, *want)
+                        assert n <= query, (M, K, N, epi, want)
+                        if not want[0] and M <= 8 and epi == S.EPI_NONE:
+                            assert n == 0
+                    # the bias's gradient alone is called without K
+                    assert need(M, 1, N, epi, False, False) <= query
+
+
 def norm(dtype=0, pt=0, M=4, K=64, X=A, ldx=64, w=B, ldw=64, b=C, ldb=64, off=0.0, rpg=2, eps=1e-6,
          Y=D, ldy=64, mean=None, rstd=None):
     return S.lib().svdq_layer_norm(dtype, pt, M, K, X, ldx, w, ldw, b, ldb, off, rpg, eps, Y, ldy, mean,

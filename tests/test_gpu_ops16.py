@@ -340,6 +340,24 @@ def test_linear_backward_parts(want, epi):
     check_linear_bwd(100, 136, 72, BF16, epi, want=want)
 
 
+@pytest.mark.parametrize("M,K,N,epi", [(8, 28672, 8192, S.EPI_NONE), (8, 28672, 8192, S.EPI_GELU), (4, 40000, 600, S.EPI_SILU),
+                                       (1, 64, 300, S.EPI_NONE), (40, 64, 300, S.EPI_NONE)])
+def test_linear_backward_of_the_bias_alone(M, K, N, epi):
+    """Without X and W the call does not know K; the workspace that the query
+    gives for the layer is enough."""
+    g = gen(M)
+    dY, P = rows(g, M, N, BF16), rows(g, M, N, BF16)
+    db, want = (torch.empty((N,), dtype=BF16, device="cuda") for _ in range(2))
+    ws = torch.full((S.svdq_linear16_backward_workspace(M, K, N, epi),), 255, dtype=torch.uint8, device="cuda")
+    S.svdq_linear16_backward(dY, None, None, P if epi else None, None, None, db, ws, epi)
+    d = dY.double() * act_grad64(P.double(), epi)
+    e = (2.0 ** -20 * dY.double().abs()).sum(0) * bool(epi) + (M + 3) * 2.0 ** -24 * d.abs().sum(0)
+    close(db, d.sum(0), half(BF16) * (d.sum(0).abs() + e) + e, "db")
+    if M <= 8 and not epi:                              # no partial sums: none is needed
+        S.svdq_linear16_backward(dY, None, None, None, None, None, want, None)
+        assert torch.equal(db, want)
+
+
 def test_linear_backward_of_an_empty_batch_is_zero():
     dW, db = out(24, 40, BF16), torch.full((24,), 77.0, dtype=BF16, device="cuda")
     e = lambda k: torch.empty((0, k), dtype=BF16, device="cuda")

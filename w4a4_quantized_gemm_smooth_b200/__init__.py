@@ -524,7 +524,7 @@ def svdq_linear16(X, W, Y, bias=None, residual=None, epilogue=EPI_NONE, preact=N
 
 
 def svdq_linear16_backward_workspace(M: int, K: int, N: int, epilogue=EPI_NONE) -> int:
-    """Workspace bytes of svdq_linear16_backward (0 for invalid arguments)."""
+    """Workspace bytes of svdq_linear16_backward (may be 0; 0 for invalid arguments)."""
     return int(lib().svdq_linear16_backward_workspace(int(M), int(K), int(N), int(epilogue)))
 
 

@@ -232,22 +232,28 @@ cudaError_t launch_gemm(G16Launch& l, cudaStream_t st) {
   return launch(l, both);
 }
 
-// Workspace of the backward call: dP, then the column sums' partials.
+// Workspace of a backward call: dP of an activation, then the partial column
+// sums of db; or, for few rows, the partial sums of dX.  What a call does not
+// ask for takes no room, so that `need` of a call is at most that of the call
+// for all three gradients, whatever K stands in the call for db alone.
 struct BwdLayout {
-  size_t dp, part, total;
+  size_t dp, part, need;
   long long lddp;
+  bool thin;
+  int row_blocks;              // of dp_kernel
 };
-BwdLayout bwd_layout(int M, int K, int N, int epilogue) {
+BwdLayout bwd_layout(int M, int K, int N, int epilogue, bool dX, bool dW, bool db) {
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
   BwdLayout L{};
-  L.lddp = ((long long)N + 7) / 8 * 8;
-  L.dp = 0;
-  L.part = epilogue == SVDQ_EPI_NONE ? 0 : up((size_t)M * L.lddp * 2);
-  L.total = L.part + up((size_t)dp_row_blocks(M, N) * N * sizeof(float));
-  if (M <= THIN_BWD_ROWS) {             // all of it is then for the sums of dX
-    const size_t thin = up(thin16_bwd_workspace(M, K, N));
-    if (thin > L.total) L.total = thin;
+  L.thin = M <= THIN_BWD_ROWS && (dX || dW);
+  if (L.thin) {
+    L.need = dX ? up(thin16_bwd_workspace(M, K, N)) : 0;
+    return L;
   }
+  L.lddp = ((long long)N + 7) / 8 * 8;
+  L.part = epilogue == SVDQ_EPI_NONE ? 0 : up((size_t)M * L.lddp * 2);
+  L.row_blocks = dp_row_blocks(M, N);
+  L.need = L.part + (db && L.row_blocks > 1 ? up((size_t)L.row_blocks * N * sizeof(float)) : 0);
   return L;
 }
 
@@ -322,7 +328,10 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
 
 size_t svdq_linear16_backward_workspace(int M, int K, int N, int epilogue) {
   if (M <= 0 || K < 1 || N < 1 || !svdq::ok_call(SVDQ_DTYPE_BF16, epilogue)) return 0;
-  return svdq::bwd_layout(M, K, N, epilogue).total;
+  // the most that any choice of gradients needs: few rows go another way for db alone
+  const size_t all = svdq::bwd_layout(M, K, N, epilogue, true, true, true).need;
+  const size_t db = svdq::bwd_layout(M, K, N, epilogue, false, false, true).need;
+  return all > db ? all : db;
 }
 
 svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* dY, int lddy,
@@ -345,21 +354,19 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
     return SVDQ_OK;
   }
   if (!dX && !dW && !db) return SVDQ_OK;
-  const bool thin = M <= svdq::THIN_BWD_ROWS && (dX || dW);
-  const bool needs_ws = act || db || (thin && dX);
-  if (!dY || (dW && !X) || (dX && !W) || (act && !P) || (needs_ws && !workspace)) return SVDQ_ERR_INVALID_ARG;
+  const svdq::BwdLayout L = svdq::bwd_layout(M, K, N, epilogue, dX, dW, db);
+  if (!dY || (dW && !X) || (dX && !W) || (act && !P) || (L.need && !workspace)) return SVDQ_ERR_INVALID_ARG;
   if (!rows_aligned16(dY, lddy, 2) || (dW && !rows_aligned16(X, ldx, 2)) ||
       (dX && (!rows_aligned16(W, ldw, 2) || !rows_aligned16(dX, lddx, 2))) ||
       (act && !rows_aligned16(P, ldp, 2)) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return SVDQ_ERR_ALIGNMENT;
-  const svdq::BwdLayout L = svdq::bwd_layout(M, K, N, epilogue);
-  if (needs_ws && workspace_bytes < L.total) return SVDQ_ERR_SHAPE;
+  if (L.need && workspace_bytes < L.need) return SVDQ_ERR_SHAPE;
   {
     using svdq::extent_rows;
     const svdq::Extent dy = extent_rows(dY, M, N, lddy, 2), x = extent_rows(dW ? X : nullptr, M, K, ldx, 2),
                        w = extent_rows(dX ? W : nullptr, N, K, ldw, 2),
                        p = extent_rows(act ? P : nullptr, M, N, ldp, 2),
-                       ws = svdq::extent_flat(needs_ws ? workspace : nullptr, (long long)L.total),
+                       ws = svdq::extent_flat(workspace, (long long)L.need),
                        gx = extent_rows(dX, M, K, lddx, 2), gw = extent_rows(dW, N, K, lddw, 2),
                        gb = svdq::extent_flat(db, 2ll * N);
     if (svdq::overlaps_any(gx, {dy, x, w, p, ws, gw, gb}) || svdq::overlaps_any(gw, {dy, x, w, p, ws, gb}) ||
@@ -367,7 +374,7 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
       return SVDQ_ERR_INVALID_ARG;
   }
   const int bf16 = dtype == SVDQ_DTYPE_BF16;
-  if (thin) {
+  if (L.thin) {
     const svdq::ThinBwdCall c{dY, act ? P : nullptr, dW ? X : nullptr, dX ? W : nullptr, dX, dW, db, workspace,
                               lddy, ldp, ldx, ldw, lddx, lddw, M, K, N, epilogue, bf16};
     return svdq::launch_thin16_bwd(c, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
@@ -388,8 +395,7 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
       dP = d.dp;
       lddp = L.lddp;
     }
-    const int want = svdq::dp_row_blocks(M, N);
-    d.rows_per_block = (int)(((long long)M + want - 1) / want);
+    d.rows_per_block = (int)(((long long)M + L.row_blocks - 1) / L.row_blocks);
     const int blocks = (int)(((long long)M + d.rows_per_block - 1) / d.rows_per_block);
     const dim3 grid((unsigned)(((long long)N + svdq::DP_COLS - 1) / svdq::DP_COLS), (unsigned)blocks);
     if (db && blocks == 1)
