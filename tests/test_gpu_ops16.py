@@ -491,6 +491,35 @@ def test_norm_constant_and_bad_rows():
     assert torch.equal(Y[[0, 1, 2, 5]], Z[[0, 1, 2, 5]])
 
 
+@pytest.mark.parametrize("K", [64, 119, 120, 125, 200, 1000, 1153, 2601, 4608, 5121, 8191, 14001])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_norm_of_constant_rows(K, dtype):
+    """Rows of one value each, whose sums are exact in fp32 (at most 11 bits
+    times K, 22 to 24 bits): the mean is the value itself and the output the
+    shift, at any length."""
+    bits = 11 if K <= 8192 else 8
+    v = torch.tensor([3.0, 100.0, 1000.0, -7.3125, 0.1015625, 255.0, 1e4, 2.0 ** -20, 0.0, -1.0, 1.0], device="cuda")
+    m, e = torch.frexp(v)
+    v = torch.ldexp((m * 2 ** bits).round(), e - bits).to(dtype)
+    X = out(len(v), K, dtype)
+    X.copy_(v[:, None].expand(-1, K))
+    w, b = torch.randn((K,), device="cuda"), torch.randn((K,), device="cuda")
+    Y, mean, rs = out(len(v), K, dtype), torch.empty((len(v),), device="cuda"), torch.empty((len(v),), device="cuda")
+    S.svdq_layer_norm(X, Y, w, b, 1e-6, mean=mean, rstd=rs)
+    assert torch.equal(mean, v.float())
+    assert torch.equal(Y, b.to(dtype).expand(len(v), K))
+    assert bool(((rs.double() * 1e-3 - 1).abs() <= 2.0 ** -22).all())        # 1 / sqrt(eps), of eps in fp32
+
+
+def test_norm_keeps_an_infinite_mean():
+    X = torch.randn((4, 256), device="cuda")[:, :250]
+    X[1, 3], X[2, 5], X[3, 7] = float("inf"), float("-inf"), float("nan")
+    Y, mean = torch.empty((4, 256), device="cuda")[:, :250], torch.empty((4,), device="cuda")
+    S.svdq_layer_norm(X, Y, mean=mean)
+    assert bool(mean[0].isfinite()) and bool(mean[1] == float("inf")) and bool(mean[2] == float("-inf"))
+    assert bool(mean[3].isnan()) and bool(Y[1:].isnan().all())
+
+
 def test_norm_of_no_rows():
     e = torch.empty((0, 64), dtype=BF16, device="cuda")
     S.svdq_layer_norm(e, e)
