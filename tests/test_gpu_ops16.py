@@ -241,6 +241,36 @@ def test_linear_activation_tails(dtype, M):
         assert bool(((db.double() - ref).abs() <= h * ref.abs() + 2.0 ** -15 * parts + tiny).all())
 
 
+@pytest.mark.parametrize("M", [16, 200])
+def test_linear_silu_to_the_least_numbers(M):
+    """SiLU and its slope where exp(-x) leaves fp32 but the result is still a
+    bf16 number, down to its least ones (steps of 2^-133), and at infinity,
+    where the slope is 1 and 0."""
+    v = torch.linspace(-104.0, -70.0, M, device="cuda").to(BF16)
+    X = torch.zeros((M, 8), dtype=BF16, device="cuda")
+    X[:, 0] = v
+    W = torch.zeros((8, 8), dtype=BF16, device="cuda")
+    W[:, 0] = 1.0
+    Y = out(M, 8, BF16)
+    S.svdq_linear16(X, W, Y, epilogue=S.EPI_SILU)
+    p = v.double()[:, None]
+    ref = act64(p, S.EPI_SILU)
+    # half a step, 2^-15 of itself for the exponential's argument, 128 roundings at fp32's least number
+    bound = lambda r, parts: half(BF16) * r.abs() + 2.0 ** -15 * parts.abs() + 2.0 ** -134 + 2.0 ** -142
+    assert bool(((Y.double() - ref).abs() <= bound(ref, ref)).all()) and bool((Y[p[:, 0] > -90] != 0).all())
+    ends = torch.tensor([float("inf"), float("-inf"), float("nan"), 3e38, -3e38, 200.0, -200.0, 0.0], device="cuda").to(BF16)
+    P = torch.cat([v, ends])[None].contiguous()
+    n = P.shape[1]
+    db = torch.empty((n,), dtype=BF16, device="cuda")
+    ws = torch.empty((S.svdq_linear16_backward_workspace(1, 8, n, S.EPI_SILU),), dtype=torch.uint8, device="cuda")
+    S.svdq_linear16_backward(torch.ones_like(P), None, None, P, None, None, db, ws, S.EPI_SILU)
+    q = torch.sigmoid(p[:, 0])
+    ref = q * (1 + p[:, 0] * (1 - q))
+    assert bool(((db[:M].double() - ref).abs() <= bound(ref, ref)).all())
+    assert db[M:M + 2].tolist() == [1.0, 0.0] and bool(db[M + 2].isnan())
+    assert db[M + 3:].tolist() == [1.0, 0.0, 1.0, 0.0, 0.5]
+
+
 def check_linear_bwd(M, K, N, dtype, epi, bias=True, seed=0, want=(True, True, True)):
     g = gen(seed)
     X, W = rows(g, M, K, dtype), rows(g, N, K, dtype, K ** -0.5)

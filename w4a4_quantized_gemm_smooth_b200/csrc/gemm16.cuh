@@ -127,6 +127,27 @@ __device__ __forceinline__ GaussTail gauss_tail(float2 x) {
   return g;
 }
 
+// For pairs: a = x clamped to +-128, t = exp(-|a|), at = a t and q = 1 / (1 + t),
+// of which x / (1 + exp(-x)) is x q or, for x < 0, a t q.  1 + t lies in [1, 2],
+// and t is the square of exp(-|a| / 2), by which `at` is formed without t, so
+// nothing overflows and the far negative side keeps its digits down to the
+// least number of the 16-bit type: a quotient by 1 + exp(-x) gave 0 from -87.4
+// on.  The exponential's argument, up to 128, in fp32 makes t right to 2^-17.
+struct LogisticTail {
+  float2 t, at, q;
+};
+__device__ __forceinline__ LogisticTail logistic_tail(float2 x) {
+  LogisticTail g;
+  const float2 a = make_float2(max_nan(min_nan(x.x, 128.0f), -128.0f), max_nan(min_nan(x.y, 128.0f), -128.0f));
+  const float2 z = __fmul2_rn(make_float2(fabsf(a.x), fabsf(a.y)), make_float2(-0.72134752f, -0.72134752f));
+  const float2 h = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+  g.t = __fmul2_rn(h, h);
+  g.at = __fmul2_rn(__fmul2_rn(a, h), h);
+  const float2 d = __fadd2_rn(g.t, make_float2(1.0f, 1.0f));
+  g.q = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  return g;
+}
+
 // The activation of two sums: GELU is x (1 - h) or, for x < 0, x h, that is
 // max(x, 0) - |x| h (|x| clamped where h is 0, so that infinity stays); SiLU
 // is x / (1 + exp(-x)).
@@ -135,11 +156,15 @@ __device__ __forceinline__ float2 g_act2(float2 x, int epilogue) {
     const GaussTail g = gauss_tail(x);
     return __ffma2_rn(make_float2(-g.a.x, -g.a.y), g.h, make_float2(max_nan(x.x, 0.0f), max_nan(x.y, 0.0f)));
   }
-  if (epilogue == SVDQ_EPI_SILU)
-    return make_float2(__fdividef(x.x, 1.0f + __expf(-x.x)), __fdividef(x.y, 1.0f + __expf(-x.y)));
+  if (epilogue == SVDQ_EPI_SILU) {
+    const LogisticTail g = logistic_tail(x);
+    return __fmul2_rn(make_float2(x.x >= 0.0f ? x.x : g.at.x, x.y >= 0.0f ? x.y : g.at.y), g.q);
+  }
   return x;
 }
-// Its derivative: GELU's is Phi(x) + x phi(x), with Phi = 1 - h, or h for x < 0.
+// Its derivative: GELU's is Phi(x) + x phi(x), with Phi = 1 - h, or h for x < 0;
+// SiLU's s + x s (1 - s) for s = 1 / (1 + exp(-x)), where s is q, or t q for
+// x < 0, and s (1 - s) is t q^2 on both sides.
 __device__ __forceinline__ float2 g_act_grad2(float2 x, int epilogue) {
   if (epilogue == SVDQ_EPI_GELU) {
     const GaussTail g = gauss_tail(x);
@@ -148,8 +173,10 @@ __device__ __forceinline__ float2 g_act_grad2(float2 x, int epilogue) {
     const float2 s = make_float2(copysignf(g.a.x, x.x), copysignf(g.a.y, x.y));
     return __ffma2_rn(__fmul2_rn(s, make_float2(0.39894228f, 0.39894228f)), g.e, up);
   }
-  const float2 q = make_float2(__fdividef(1.0f, 1.0f + __expf(-x.x)), __fdividef(1.0f, 1.0f + __expf(-x.y)));
-  return make_float2(q.x * (1.0f + x.x * (1.0f - q.x)), q.y * (1.0f + x.y * (1.0f - q.y)));
+  const LogisticTail g = logistic_tail(x);
+  const float2 u = __fmul2_rn(g.t, g.q);
+  const float2 s = make_float2(x.x < 0.0f ? u.x : g.q.x, x.y < 0.0f ? u.y : g.q.y);
+  return __ffma2_rn(__fmul2_rn(g.at, g.q), g.q, s);
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t u, bool bf16) {
