@@ -1098,6 +1098,54 @@ def test_two_graphs_on_forked_streams():
         assert torch.equal(Z, want) and torch.equal(N, wantn) and torch.equal(Y, want + want)
 
 
+def test_a_failed_call_leaves_no_error_behind():
+    """The runtime remembers the last error until it is read: a call that
+    answers with a status must not leave it to the next check of a launch.  A
+    capture into which a synchronisation came takes no more launches."""
+    g = gen(62)
+    X, W, P = rows(g, 40, 64, BF16), rows(g, 48, 64, BF16), rows(g, 40, 48, BF16)
+    Y, dX, dW, N, db = (torch.empty(s, dtype=BF16, device="cuda") for s in ((40, 48), (40, 64), (48, 64), (40, 64), (48,)))
+    need = max(S.svdq_linear16_backward_workspace(m, 64, 48, S.EPI_GELU) for m in (4, 40))
+    ws = torch.empty((need,), dtype=torch.uint8, device="cuda")
+    mean, rs = torch.zeros((40,), device="cuda"), torch.ones((40,), device="cuda")
+    plan, pos = S.svdq_rope_create([4], [1.0] * 4), torch.zeros((40, 1), dtype=torch.int32, device="cuda")
+    path = next(line.split()[-1] for line in open("/proc/self/maps") if "libcudart" in line)
+    rt = ctypes.CDLL(path)
+    side = torch.cuda.Stream()
+    calls = [
+        lambda st: S.svdq_linear16(X, W, Y, stream=st),
+        lambda st: S.svdq_linear16(X[:4], W, Y[:4], stream=st),
+        lambda st: S.svdq_linear16_backward(P, X, W, P, dX, dW, db, ws, S.EPI_GELU, stream=st),
+        lambda st: S.svdq_linear16_backward(P[:4], X[:4], W, P[:4], dX[:4], dW, db, ws, S.EPI_GELU, stream=st),
+        lambda st: S.svdq_layer_norm(X, N, stream=st),
+        lambda st: S.svdq_layer_norm_backward(X, X, mean, rs, N, stream=st),
+        lambda st: S.svdq_rope(plan, pos, X.unflatten(1, (4, 16)), N.unflatten(1, (4, 16)), stream=st),
+    ]
+    for call in calls:
+        call(None)
+    torch.cuda.synchronize()
+    assert rt.cudaPeekAtLastError() == 0
+    handle, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    assert rt.cudaStreamBeginCapture(handle, 2) == 0            # relaxed
+    try:
+        with pytest.raises(S.SVDQError) as e:
+            S.svdq_get_op_error(side)                           # synchronises
+        left = [("svdq_get_op_error", e.value.status, rt.cudaPeekAtLastError())]
+        for i, call in enumerate(calls):
+            with pytest.raises(S.SVDQError) as e:
+                call(side)
+            left.append((i, e.value.status, rt.cudaPeekAtLastError()))
+    finally:
+        rt.cudaStreamEndCapture(handle, ctypes.byref(graph))
+        rt.cudaGetLastError()
+    assert [(s, p) for _, s, p in left] == [(6, 0)] * len(left), left
+    S.svdq_linear16(X, W, Y)
+    ref = X.double() @ W.double().T
+    err = 65 * 2.0 ** -24 * (X.double().abs() @ W.double().abs().T)
+    close(Y, ref, half(BF16) * (ref.abs() + err) + err)
+    S.svdq_get_op_error()
+
+
 def test_slices_of_one_buffer_are_no_overlap():
     """Inputs and outputs that interleave in one buffer are taken, and give
     what separate arrays give; an output over an input is refused."""

@@ -836,7 +836,7 @@ svdq_status svdq_layer_norm(int dtype, int param_dtype, int M, int K, const void
   const cudaError_t e = svdq::dispatch_types(dtype, param_dtype, [&](auto t, auto pt) {
     return svdq::fwd<decltype(t), decltype(pt)>(a, stream);
   });
-  return e == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  return svdq::status_of(e);
 }
 
 size_t svdq_layer_norm_backward_workspace(int M, int K, int rows_per_group) {
@@ -865,10 +865,9 @@ svdq_status svdq_layer_norm_backward(int dtype, int param_dtype, int M, int K, c
     return SVDQ_ERR_ALIGNMENT;
   if (M == 0) {
     if (rows_per_group) return SVDQ_OK;
-    if ((dweight && cudaMemsetAsync(dweight, 0, (size_t)K * ps, stream) != cudaSuccess) ||
-        (dbias && cudaMemsetAsync(dbias, 0, (size_t)K * ps, stream) != cudaSuccess))
-      return SVDQ_ERR_CUDA;
-    return SVDQ_OK;
+    cudaError_t e = dweight ? cudaMemsetAsync(dweight, 0, (size_t)K * ps, stream) : cudaSuccess;
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)K * ps, stream);
+    return svdq::status_of(e);
   }
   if (!dY || !X || !mean || !rstd || (dX == dY && lddx != lddy) || (dX == X && lddx != ldx))
     return SVDQ_ERR_INVALID_ARG;
@@ -907,7 +906,7 @@ svdq_status svdq_layer_norm_backward(int dtype, int param_dtype, int M, int K, c
   const cudaError_t e = svdq::dispatch_types(dtype, param_dtype, [&](auto t, auto pt) {
     return svdq::bwd<decltype(t), decltype(pt)>(a, stream);
   });
-  return e == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  return svdq::status_of(e);
 }
 
 }  // extern "C"

@@ -322,8 +322,8 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
   o.M = M;
   o.N = N;
   if (M <= svdq::THIN_ROWS)
-    return svdq::launch_thin16(X, ldx, W, ldw, K, o, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
-  return svdq::launch_gemm(l, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+    return svdq::status_of(svdq::launch_thin16(X, ldx, W, ldw, K, o, stream));
+  return svdq::status_of(svdq::launch_gemm(l, stream));
 }
 
 size_t svdq_linear16_backward_workspace(int M, int K, int N, int epilogue) {
@@ -348,10 +348,9 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
   if ((dW && !rows_aligned16(dW, lddw, 2)) || (db && (reinterpret_cast<uintptr_t>(db) & 1)))
     return SVDQ_ERR_ALIGNMENT;
   if (M == 0) {
-    if ((dW && cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)K * 2, N, stream) != cudaSuccess) ||
-        (db && cudaMemsetAsync(db, 0, (size_t)N * 2, stream) != cudaSuccess))
-      return SVDQ_ERR_CUDA;
-    return SVDQ_OK;
+    cudaError_t e = dW ? cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)K * 2, N, stream) : cudaSuccess;
+    if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, (size_t)N * 2, stream);
+    return svdq::status_of(e);
   }
   if (!dX && !dW && !db) return SVDQ_OK;
   const svdq::BwdLayout L = svdq::bwd_layout(M, K, N, epilogue, dX, dW, db);
@@ -377,7 +376,7 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
   if (L.thin) {
     const svdq::ThinBwdCall c{dY, act ? P : nullptr, dW ? X : nullptr, dX ? W : nullptr, dX, dW, db, workspace,
                               lddy, ldp, ldx, ldw, lddx, lddw, M, K, N, epilogue, bf16};
-    return svdq::launch_thin16_bwd(c, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+    return svdq::status_of(svdq::launch_thin16_bwd(c, stream));
   }
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const void* dP = dY;
@@ -405,10 +404,10 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
     auto kernel = epilogue == SVDQ_EPI_GELU   ? svdq::dp_kernel<SVDQ_EPI_GELU>
                   : epilogue == SVDQ_EPI_SILU ? svdq::dp_kernel<SVDQ_EPI_SILU>
                                               : svdq::dp_kernel<SVDQ_EPI_NONE>;
-    if (svdq::launch_op(kernel, grid, 256, 0, 1, stream, d) != cudaSuccess) return SVDQ_ERR_CUDA;
-    if (d.part && svdq::launch_join(d.part, blocks, 1, N, N, static_cast<uint16_t*>(db), 0, bf16,
-                                    stream) != cudaSuccess)
-      return SVDQ_ERR_CUDA;
+    cudaError_t e = svdq::launch_op(kernel, grid, 256, 0, 1, stream, d);
+    if (e == cudaSuccess && d.part)
+      e = svdq::launch_join(d.part, blocks, 1, N, N, static_cast<uint16_t*>(db), 0, bf16, stream);
+    if (e != cudaSuccess) return svdq::status_of(e);
   }
   svdq::G16Launch l{};
   l.kind = svdq::G16Kind::Gradients;
@@ -423,24 +422,20 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
   };
   if (dX) set(0, {dP, lddp, M, N, false}, {W, ldw, K, N, true}, dX, lddx);
   if (dW) set(1, {dP, lddp, N, M, true}, {X, ldx, K, M, true}, dW, lddw);
-  if ((dX || dW) && svdq::launch_gemm(l, stream) != cudaSuccess) return SVDQ_ERR_CUDA;
-  return SVDQ_OK;
+  return svdq::status_of(dX || dW ? svdq::launch_gemm(l, stream) : cudaSuccess);
 }
 
 svdq_status svdq_get_op_error(cudaStream_t stream) {
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return SVDQ_ERR_CUDA;
+  cudaError_t e = cudaStreamSynchronize(stream);
   int v = 0;
   const int zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&v, svdq::g_op_err, sizeof(int), 0, cudaMemcpyDeviceToHost,
-                                stream) != cudaSuccess ||
-      cudaStreamSynchronize(stream) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  if (v == SVDQ_DEVERR_NONE) return SVDQ_OK;
-  if (cudaMemcpyToSymbolAsync(svdq::g_op_err, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
-                              stream) != cudaSuccess ||
-      cudaStreamSynchronize(stream) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  return SVDQ_ERR_DEVICE_TIMEOUT;
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(&v, svdq::g_op_err, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess || v == SVDQ_DEVERR_NONE) return svdq::status_of(e);
+  e = cudaMemcpyToSymbolAsync(svdq::g_op_err, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  return e == cudaSuccess ? SVDQ_ERR_DEVICE_TIMEOUT : svdq::status_of(e);
 }
 
 }  // extern "C"

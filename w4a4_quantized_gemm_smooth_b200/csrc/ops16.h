@@ -48,6 +48,16 @@ cudaError_t launch_op(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// The status of a CUDA result.  The runtime keeps a failed call's error for the
+// thread until it is read; it is read here, since the call answers with its
+// status and the next check of a launch, the library's or its user's, would
+// take the old error for its own.
+inline svdq_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return SVDQ_OK;
+  (void)cudaGetLastError();
+  return SVDQ_ERR_CUDA;
+}
+
 inline int dtype_size(int dtype) { return dtype == SVDQ_DTYPE_F32 ? 4 : 2; }
 
 }  // namespace svdq

@@ -318,9 +318,8 @@ svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int hea
     if ((X != Y && svdq::overlap(y, extent(X, ldx_token, ldx_head))) || svdq::overlap(y, pos))
       return SVDQ_ERR_INVALID_ARG;
   }
-  return svdq::launch_rope(plan, dtype, tokens, heads, head_dim, positions, pos_rows, ld_pos, X,
-                           ldx_token, ldx_head, Y, ldy_token, ldy_head, inverse,
-                           stream) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  return svdq::status_of(svdq::launch_rope(plan, dtype, tokens, heads, head_dim, positions, pos_rows, ld_pos, X,
+                                           ldx_token, ldx_head, Y, ldy_token, ldy_head, inverse, stream));
 }
 
 }  // extern "C"
