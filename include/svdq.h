@@ -667,7 +667,8 @@ void svdq_rope_free(svdq_rope_plan* plan);
  * stride or all tokens within a head's (else SVDQ_ERR_SHAPE); Y may be X with
  * equal strides (in place).  positions: device int32 [pos_rows][ld_pos], one
  * column per axis, any sign; token t uses row t % pos_rows (images of one
- * size in a batch share their positions).  Queries and keys side by side in
+ * size in a batch share their positions; pos_rows >= 1 unless there is no
+ * token).  Queries and keys side by side in
  * the rows of a fused QKV product are one call over their heads.
  */
 svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int heads,

@@ -199,6 +199,12 @@ def test_rope_refusals():
     S.lib().svdq_rope_free(h)
 
 
+def test_rope_of_no_tokens_takes_no_positions():
+    p = S.svdq_rope_create([2], [1.0, 0.5])
+    call = lambda T, rows: S.lib().svdq_rope(p.handle, 0, T, 2, 8, None, rows, 1, None, 16, 8, None, 16, 8, 0, None)
+    assert call(0, 0) == OK and call(0, 5) == OK and call(0, -1) == SHAPE and call(1, 0) == SHAPE
+
+
 # an output that shares memory with another array of its call: blocks run in any
 # order, so the result would depend on timing
 def test_linear16_refuses_overlap():

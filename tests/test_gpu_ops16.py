@@ -822,6 +822,13 @@ def test_rope_many_heads_and_tokens():
     check_rope(70000, 1, 8, (1, 1), S.ROPE_INTERLEAVED, F16)
 
 
+def test_rope_of_no_tokens():
+    plan = S.svdq_rope_create([2, 2], S.rope_frequencies([2, 2]))
+    X = torch.empty((0, 3, 8), dtype=BF16, device="cuda")
+    S.svdq_rope(plan, torch.empty((0, 2), dtype=torch.int32, device="cuda"), X, X)
+    S.svdq_rope(plan, torch.zeros((4, 2), dtype=torch.int32, device="cuda"), X, torch.empty_like(X))
+
+
 def test_rope_copies_what_it_does_not_turn():
     """NaN and infinity past the pairs pass through; inside a pair they stay in it."""
     X = torch.randn((4, 2, 24), device="cuda").to(BF16)

@@ -286,7 +286,7 @@ svdq_status svdq_rope(const svdq_rope_plan* plan, int dtype, int tokens, int hea
                       long long ldx_token, long long ldx_head, void* Y, long long ldy_token,
                       long long ldy_head, int inverse, cudaStream_t stream) {
   if (!plan || dtype < SVDQ_DTYPE_BF16 || dtype > SVDQ_DTYPE_F32) return SVDQ_ERR_INVALID_ARG;
-  if (tokens < 0 || heads < 0 || pos_rows < 1 || ld_pos < plan->t.axes || head_dim < 2 ||
+  if (tokens < 0 || heads < 0 || pos_rows < (tokens ? 1 : 0) || ld_pos < plan->t.axes || head_dim < 2 ||
       head_dim % 2 != 0 || head_dim < 2 * plan->t.pairs || ldx_token < 0 || ldx_head < 0 ||
       ldy_token < 0 || ldy_head < 0)
     return SVDQ_ERR_SHAPE;
