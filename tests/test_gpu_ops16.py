@@ -810,6 +810,47 @@ def test_rope_far_positions(pairing, dtype):
     check_rope(64, 2, 16, (4, 4), pairing, dtype, far=2 ** 20, freq=[1.0, -2.5, 3e-9, 0.0, 100.0, 7.5, 1e-3, 6.0])
 
 
+def exact_angles(pos, freq):
+    """pos freq modulo 2 pi as fp64, [positions, pairs], from integers: 2 pi to
+    400 bits by Machin's formula."""
+    from fractions import Fraction
+    one = 1 << 420
+
+    def arctan_inverse(x):
+        total = term = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            sign, n = -sign, n + 2
+        return total
+
+    two_pi = Fraction(8 * (4 * arctan_inverse(5) - arctan_inverse(239)), one)
+    return torch.tensor([[float(Fraction(f) * p % two_pi) for f in freq] for p in pos], dtype=torch.float64)
+
+
+@pytest.mark.parametrize("pairing", [S.ROPE_INTERLEAVED, S.ROPE_HALVES])
+def test_rope_large_frequencies_at_far_positions(pairing):
+    """The angle of any position is exact modulo a turn for any frequency that
+    a plan takes, not only for those up to 1."""
+    freq = [1.0, -1.0, 3.7e3, -65535.9, 1048575.9, 523456.789, 1e-9, 2.0 ** 19 / 3]
+    pos = [0, 1, -1, 7, 12345, -99999, 2 ** 24 + 1, 2 ** 30 + 12347, 2 ** 31 - 1, -2 ** 31]
+    g = gen(71)
+    X = torch.randn((len(pos), 2, 2 * len(freq)), generator=g, device="cuda")
+    Y = torch.empty_like(X)
+    plan = S.svdq_rope_create([len(freq)], freq, pairing)
+    S.svdq_rope(plan, torch.tensor(pos, device="cuda").to(torch.int32)[:, None], X, Y)
+    ang = exact_angles(pos, freq).cuda()
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+    n = len(freq)
+    ia, ib = ((slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if pairing == S.ROPE_INTERLEAVED
+              else (slice(0, n), slice(n, 2 * n)))
+    a, b = X[..., ia].double(), X[..., ib].double()
+    mag = 2.0 ** -22 * (a.abs() + b.abs())
+    close(Y[..., ia], a * c - b * s, half(F32) * mag + mag, "first")
+    close(Y[..., ib], a * s + b * c, half(F32) * mag + mag, "second")
+
+
 @pytest.mark.parametrize("inplace", [False, True])
 def test_rope_shared_positions_and_in_place(inplace):
     check_rope(60, 6, 72, (12, 12, 12), S.ROPE_HALVES, BF16, prows=15, inplace=inplace, pad=216)

@@ -225,6 +225,27 @@ cudaError_t launch_t(const svdq_rope_plan* plan, const RopeArgs& a, int tokens, 
 
 }  // namespace
 
+// Fraction of a turn, times 2^64 and modulo that, of `freq` radians (below 2^20
+// in magnitude), to the nearest: freq = m 2^e with a 53-bit m and e <= -33, and
+// m / 2 pi comes from the first 128 bits of 1 / 2 pi in integers, so that the
+// error before the last rounding is below 2^53 2^-128 2^e, whatever the size.
+uint64_t turn_of(double freq) {
+  // floor(2^128 / 2 pi)
+  constexpr unsigned __int128 INV_2PI = (unsigned __int128)0x28BE60DB9391054Aull << 64 | 0x7F09D5F47D4D3770ull;
+  int exp = 0;
+  const double frac = std::frexp(std::fabs(freq), &exp);             // freq = frac 2^exp
+  const uint64_t m = (uint64_t)std::ldexp(frac, 53);
+  // m INV_2PI is the turns times 2^(128 - e), e = exp - 53; `high` leaves out its
+  // last 64 bits, so that the result's last bit is bit -e of it, 33 or more
+  const unsigned __int128 low = (unsigned __int128)m * (uint64_t)INV_2PI;
+  const unsigned __int128 high = (unsigned __int128)m * (uint64_t)(INV_2PI >> 64) + (uint64_t)(low >> 64);
+  const int shift = 53 - exp;
+  if (frac == 0.0 || shift > 128) return 0;                          // below half of the last bit
+  const unsigned __int128 half = (high >> (shift - 1)) + 1;
+  const uint64_t turn = (uint64_t)(half >> 1);
+  return freq < 0.0 ? 0 - turn : turn;
+}
+
 cudaError_t launch_rope(const svdq_rope_plan* plan, int dtype, int tokens, int heads,
                         int head_dim, const int32_t* pos, int pos_rows, int ld_pos, const void* X,
                         long long ldxt, long long ldxh, void* Y, long long ldyt, long long ldyh,
@@ -268,12 +289,7 @@ svdq_status svdq_rope_create(int n_axes, const int* pairs_per_axis, const double
   for (int a = 0; a < n_axes; ++a)
     for (int j = 0; j < pairs_per_axis[a]; ++j, ++p) {
       plan->t.axis[p] = (uint8_t)a;
-      // fraction of a turn in [0, 1) times 2^64, in 64-bit-mantissa arithmetic
-      const long double two_pi = 6.283185307179586476925286766559005768L;
-      long double f = (long double)freq[p] / two_pi;
-      f -= floorl(f);
-      const long double scaled = floorl(ldexpl(f, 64) + 0.5L);
-      plan->t.turn[p] = scaled >= ldexpl(1.0L, 64) ? 0ull : (uint64_t)scaled;
+      plan->t.turn[p] = svdq::turn_of(freq[p]);
     }
   *out = plan;
   return SVDQ_OK;
