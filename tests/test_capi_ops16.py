@@ -3,6 +3,7 @@ returned before anything touches a GPU, empty calls succeed, workspace
 queries are consistent, and the binding rejects unfit tensors."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -298,6 +299,22 @@ def test_norm_layer_refuses_to_save_what_it_overwrites():
         norm.forward(norm.Y, save=True)
     with pytest.raises(RuntimeError):
         norm.backward(x)
+
+
+def test_binding_module_is_named_for_its_interpreter(tmp_path, monkeypatch):
+    """A module that another interpreter's build left is not taken for this one's."""
+    import sysconfig
+    from w4a4_quantized_gemm_smooth_b200 import build
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert suffix.count(".") == 2                       # .cpython-3xx-<platform>.so
+    assert os.path.basename(build.FASTCALL) == "_svdq_fastcall" + suffix
+    monkeypatch.setattr(S, "_fast", None)
+    assert S._fastcall().__file__ == build.FASTCALL
+    (tmp_path / "_svdq_fastcall.so").write_bytes(b"another one's")
+    monkeypatch.setattr(S, "_fast", None)
+    monkeypatch.setattr(build, "FASTCALL", str(tmp_path / ("_svdq_fastcall" + suffix)))
+    with pytest.raises(RuntimeError, match="missing"):
+        S._fastcall()
 
 
 def test_rope_frequencies():

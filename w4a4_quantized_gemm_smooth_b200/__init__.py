@@ -492,14 +492,14 @@ _fast = None
 
 
 def _fastcall():
-    """The CPython binding (_lib/_svdq_fastcall.so, built with the library).
-    Raises if it is missing."""
+    """The CPython binding (_svdq_fastcall in _lib, built with the library for
+    the interpreter that runs).  Raises if it is missing."""
     global _fast
     if _fast is None:
         import importlib.util
         import torch
         lib()
-        path = os.path.join(_PKG, "_lib", "_svdq_fastcall.so")
+        from .build import FASTCALL as path
         if not os.path.exists(path):
             raise RuntimeError(
                 f"{path} is missing: build it with "

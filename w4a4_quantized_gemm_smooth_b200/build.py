@@ -7,7 +7,8 @@ arch=compute_100a,code=sm_100a -lineinfo -O3) and linked into
 w4a4_quantized_gemm_smooth_b200/_lib/libsvdq.so.  nvcc cross-compiles; no GPU
 is needed.  Objects go to _build/ at the repository root and are rebuilt
 only when a source or header is newer.  pyext/fastcall.c becomes
-_lib/_svdq_fastcall.so, the CPython binding of the shortest calls.
+_lib/_svdq_fastcall with the running interpreter's suffix, the CPython binding
+of the shortest calls.
 """
 from __future__ import annotations
 
@@ -28,7 +29,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libsvdq.so")
 FASTCALL_SRC = os.path.join(PKG, "pyext", "fastcall.c")
-FASTCALL = os.path.join(LIB_DIR, "_svdq_fastcall.so")
+# named for the interpreter it is built for: another one builds its own beside it
+FASTCALL = os.path.join(LIB_DIR, "_svdq_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 HOST_FLAGS = "-fPIC,-fopenmp,-O3,-ffp-contract=off,-fno-fast-math"
