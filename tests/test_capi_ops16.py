@@ -317,6 +317,34 @@ def test_binding_module_is_named_for_its_interpreter(tmp_path, monkeypatch):
         S._fastcall()
 
 
+@pytest.mark.parametrize("how", ["no gcc", "no headers"])
+def test_library_builds_without_the_binding_module(tmp_path, monkeypatch, capfd, how):
+    """The quantised layers do not need the module: the build reports that it
+    is missing, leaves no older one, and the operators raise when called."""
+    from w4a4_quantized_gemm_smooth_b200 import build
+    at = tmp_path / "_svdq_fastcall.so"
+    at.write_bytes(b"an older build's")
+    os.utime(at, (0, 0))
+    monkeypatch.setattr(build, "FASTCALL", str(at))
+    run = build.subprocess.run
+
+    def without(cmd, **kw):
+        if cmd[0] != "gcc":
+            return run(cmd, **kw)
+        if how == "no gcc":
+            raise FileNotFoundError(2, "No such file or directory", "gcc")
+        headers = build.sysconfig.get_paths()["include"]
+        return run([str(tmp_path) if c == headers else c for c in cmd], **kw)
+
+    monkeypatch.setattr(build.subprocess, "run", without)
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert not at.exists()
+    assert "16-bit operators" in capfd.readouterr().err
+    monkeypatch.setattr(S, "_fast", None)
+    with pytest.raises(RuntimeError, match="missing"):
+        S._fastcall()
+
+
 def test_rope_frequencies():
     assert S.rope_frequencies([2, 4], 100.0) == pytest.approx(
         [1.0, 0.1, 1.0, 100.0 ** -0.25, 0.1, 100.0 ** -0.75], rel=1e-15)

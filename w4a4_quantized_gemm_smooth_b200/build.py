@@ -91,20 +91,36 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stdout.write(res.stdout)
             sys.stderr.write(res.stderr)
             raise RuntimeError("link of libsvdq.so failed")
-    deps = [FASTCALL_SRC, os.path.join(INCLUDE, "svdq.h")]
-    if force or not os.path.exists(FASTCALL) or os.path.getmtime(FASTCALL) < _newest(deps):
-        cmd = ["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
-               "-I", sysconfig.get_paths()["include"], FASTCALL_SRC, "-o", FASTCALL,
-               "-L", LIB_DIR, "-lsvdq", "-Wl,-rpath,$ORIGIN"]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if verbose or res.returncode != 0:
-            sys.stdout.write(res.stdout)
-            sys.stderr.write(res.stderr)
-        if res.returncode != 0:
-            raise RuntimeError("gcc failed on fastcall.c")
+    build_fastcall(force, verbose)
     return LIB
+
+
+def build_fastcall(force: bool = False, verbose: bool = False) -> bool:
+    """Build the CPython binding of the 16-bit operators.  It wants gcc and the
+    interpreter's headers; without them the library and the quantised layers
+    work all the same, so a failure is reported and not raised: the first call
+    of a 16-bit operator raises, and no module of an older build is left."""
+    deps = [FASTCALL_SRC, os.path.join(INCLUDE, "svdq.h")]
+    if not force and os.path.exists(FASTCALL) and os.path.getmtime(FASTCALL) >= _newest(deps):
+        return True
+    cmd = ["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], FASTCALL_SRC, "-o", FASTCALL,
+           "-L", LIB_DIR, "-lsvdq", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        ok, said = res.returncode == 0, res.stdout + res.stderr
+    except OSError as e:
+        ok, said = False, f"{e}\n"
+    if verbose or not ok:
+        sys.stderr.write(said)
+    if not ok:
+        if os.path.exists(FASTCALL):
+            os.remove(FASTCALL)
+        sys.stderr.write(f"{os.path.basename(FASTCALL)} was not built: the 16-bit operators cannot be "
+                         "called from Python (gcc and Python's headers build it)\n")
+    return ok
 
 
 def main():
