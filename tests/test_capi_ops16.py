@@ -345,6 +345,15 @@ def test_library_builds_without_the_binding_module(tmp_path, monkeypatch, capfd,
         S._fastcall()
 
 
+def test_binding_does_without_torchs_private_functions(monkeypatch):
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(S, "_fast", None)
+    x = torch.zeros((4, 8), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        S.svdq_layer_norm(x, x.clone())
+
+
 def test_rope_frequencies():
     assert S.rope_frequencies([2, 4], 100.0) == pytest.approx(
         [1.0, 0.1, 1.0, 100.0 ** -0.25, 0.1, 100.0 ** -0.75], rel=1e-15)

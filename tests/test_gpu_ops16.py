@@ -985,6 +985,29 @@ def test_calls_from_other_threads_and_streams():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_binding_through_torchs_public_functions():
+    """The calls find the device and the current stream through what stands in
+    for the private functions where a torch lacks them."""
+    g = gen(24)
+    X, W = rows(g, 5, 64, BF16), rows(g, 48, 64, BF16)
+    Y, Z = out(5, 48, BF16), out(5, 48, BF16)
+    S.svdq_linear16(X, W, Y)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    S._fastcall().init((BF16, F16, F32), torch.int32, torch.cuda.current_device,
+                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    try:
+        with torch.cuda.graph(graph, stream=side):          # lands in the capture: the current stream is the one
+            S.svdq_linear16(X, W, Z)
+        assert bool((Z == 77).all())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, Z)
+    finally:
+        S._fast = None                                      # the module's functions are set anew
+        S._fastcall()
+
+
 def test_status_codes_reach_python():
     X = torch.zeros((4, 64), dtype=BF16, device="cuda")
     W = torch.zeros((8, 64), dtype=BF16, device="cuda")

@@ -507,8 +507,11 @@ def _fastcall():
         spec = importlib.util.spec_from_file_location("_svdq_fastcall", path)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
-        mod.init((torch.bfloat16, torch.float16, torch.float32), torch.int32,
-                 torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        # torch's own short cuts where it has them, else what they stand for
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                  or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        mod.init((torch.bfloat16, torch.float16, torch.float32), torch.int32, device, stream)
         _fast = mod
     return _fast
 
