@@ -985,6 +985,20 @@ def test_calls_from_other_threads_and_streams():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_epilogue_past_32_bits_is_refused():
+    X, W = torch.zeros((4, 64), dtype=BF16, device="cuda"), torch.zeros((8, 64), dtype=BF16, device="cuda")
+    Y, db = torch.zeros((4, 8), dtype=BF16, device="cuda"), torch.zeros((8,), dtype=BF16, device="cuda")
+    for epi in (1 << 32, (1 << 32) + 1, -(1 << 32)):
+        with pytest.raises(S.SVDQError) as e:
+            S.svdq_linear16(X, W, Y, epilogue=epi)
+        assert e.value.status == 1
+        with pytest.raises(S.SVDQError) as e:
+            S.svdq_linear16_backward(Y, None, None, None, None, None, db, None, epi)
+        assert e.value.status == 1
+    with pytest.raises(OverflowError):
+        S.svdq_linear16(X, W, Y, epilogue=1 << 64)
+
+
 def test_binding_through_torchs_public_functions():
     """The calls find the device and the current stream through what stands in
     for the private functions where a torch lacks them."""

@@ -97,6 +97,14 @@ static int read_stream(PyObject *o, int dev, cudaStream_t *st) {
   return PyErr_Occurred() ? -1 : 0;
 }
 
+/* An epilogue as the C calls take it: what is no int is none of them (-1). */
+static int read_epilogue(PyObject *o, int *epi) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) return -1;
+  *epi = v == (int)v ? (int)v : -1;
+  return 0;
+}
+
 /* A leading dimension as the C calls take it. */
 static int pitch(long long v) { return v < -0x7FFFFFFFll || v > 0x7FFFFFFFll ? -1 : (int)v; }
 
@@ -185,7 +193,7 @@ static int read_sizes(const Tensor *x, const char *name) {
 static PyObject *linear16(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   Tensor x, w;
   void *xp, *wp, *yp, *b, *r, *p;
-  int ldx, ldw, ldy, ldr, ldp;
+  int ldx, ldw, ldy, ldr, ldp, epi;
   cudaStream_t st;
   svdq_status rc;
   if (!nargs_are(n, 8) || read_tensor(a[0], "X", &x) < 0 || check_dtype(&x, "X") < 0 ||
@@ -193,8 +201,7 @@ static PyObject *linear16(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       read_sizes(&w, "W") < 0)
     return NULL;
   const long long M = x.shape[0], K = x.shape[1], N = w.shape[0];
-  const long epi = PyLong_AsLong(a[5]);
-  if (epi == -1 && PyErr_Occurred()) return NULL;
+  if (read_epilogue(a[5], &epi) < 0) return NULL;
   if (w.shape[1] != K || w.code != x.code || w.dev != x.dev || (K > 1 && (w.stride[1] != 1 || x.stride[1] != 1))) {
     PyErr_SetString(PyExc_ValueError, "X, W: expected [M, K] and [N, K] of one type and device with contiguous rows");
     return NULL;
@@ -213,7 +220,7 @@ static PyObject *linear16(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       read_matrix(a[6], "preact", M, N, &x, &p, &ldp) < 0)
     return NULL;
   Py_BEGIN_ALLOW_THREADS
-  rc = svdq_linear16(x.code, (int)M, (int)K, (int)N, xp, ldx, wp, ldw, b, r, ldr, (int)epi, yp, ldy, p,
+  rc = svdq_linear16(x.code, (int)M, (int)K, (int)N, xp, ldx, wp, ldw, b, r, ldr, epi, yp, ldy, p,
                      ldp, st);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
@@ -290,7 +297,7 @@ static int read_workspace(PyObject *o, int dev, void **ptr, size_t *bytes) {
 static PyObject *linear16_backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   Tensor d, t;
   void *x, *w, *p, *gx, *gw, *gb, *ws;
-  int ldd, ldx, ldw, ldp, ldgx, ldgw;
+  int ldd, ldx, ldw, ldp, ldgx, ldgw, epi;
   size_t bytes;
   cudaStream_t st;
   svdq_status rc;
@@ -304,8 +311,7 @@ static PyObject *linear16_backward(PyObject *self, PyObject *const *a, Py_ssize_
     if (read_tensor(with_k, "X, W", &t) < 0 || read_sizes(&t, "X, W") < 0) return NULL;
     K = t.shape[1];
   }
-  const long epi = PyLong_AsLong(a[8]);
-  if (epi == -1 && PyErr_Occurred()) return NULL;
+  if (read_epilogue(a[8], &epi) < 0) return NULL;
   if (N > 1 && d.stride[1] != 1) {
     PyErr_SetString(PyExc_ValueError, "dY: rows have to be contiguous");
     return NULL;
@@ -319,7 +325,7 @@ static PyObject *linear16_backward(PyObject *self, PyObject *const *a, Py_ssize_
       read_workspace(a[7], d.dev, &ws, &bytes) < 0)
     return NULL;
   Py_BEGIN_ALLOW_THREADS
-  rc = svdq_linear16_backward(d.code, (int)M, (int)K, (int)N, d.ptr, ldd, x, ldx, w, ldw, p, ldp, (int)epi,
+  rc = svdq_linear16_backward(d.code, (int)M, (int)K, (int)N, d.ptr, ldd, x, ldx, w, ldw, p, ldp, epi,
                               gx, ldgx, gw, ldgw, gb, ws, bytes, st);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
