@@ -583,6 +583,17 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
  * svdq_linear16 kernel expired on this device since the last read. */
 svdq_status svdq_get_op_error(cudaStream_t stream);
 
+/*
+ * Test hook, host only: the form in which a 16-bit product of these sizes
+ * runs.  gradients: 0 for svdq_linear16, else which of svdq_linear16_backward's
+ * are asked for (1: dX, 2: dW, 3: both).  For each launch of tensor-core tiles
+ * forms[i] = {on CTA pairs (1) or single CTAs (0), columns of a tile, CTAs that
+ * divide a tile's reduction}.  Returns the number of these launches: 1, 2 (dX
+ * and dW in a form each), or 0 for the few rows that take another way and for
+ * invalid arguments.
+ */
+int svdq_debug_linear16_forms(int M, int K, int N, int gradients, int forms[2][3]);
+
 #define SVDQ_NORM_MAX_K 16384
 
 /*

@@ -105,6 +105,28 @@ def test_linear16_backward_workspace_of_each_choice():
                     assert need(M, 1, N, epi, False, False) <= query
 
 
+def test_form_sizes_reach_every_form():
+    """Every instantiation of the tiled products (on pairs or clusters, tile
+    width, splits, forward or gradients, one problem or two) is chosen for one
+    of the sizes that the GPU tests run."""
+    from test_gpu_ops16 import FORM_SIZES
+    forms = {w: [S.svdq_debug_linear16_forms(*size, w) for size in sizes] for w, sizes in FORM_SIZES.items()}
+    one = {w: {f[0] for f in fs if len(f) == 1} for w, fs in forms.items()}
+    split = lambda widths: {(False, bn, s) for bn in widths for s in (1, 2, 4, 8) if bn // s >= 8}
+    assert one[0] == split((32, 64, 128)) | {(True, bn, 1) for bn in (128, 192, 256)}
+    grad = split((64, 128)) | {(True, bn, 1) for bn in (128, 256)}
+    assert one[1] == grad and one[2] == grad
+    # eight CTAs to a 128-wide tile of both: another form or two launches are always ahead of it
+    assert one[3] == grad - {(False, 128, 8)}
+    two = [f for f in forms[3] if len(f) == 2]
+    assert len(two) >= 15 and {f[0] for f in two} | {f[1] for f in two} == grad
+    # few rows take another way, and so does nothing else
+    assert S.svdq_debug_linear16_forms(16, 64, 64) == [] and len(S.svdq_debug_linear16_forms(17, 64, 64)) == 1
+    assert S.svdq_debug_linear16_forms(8, 64, 64, 3) == [] and len(S.svdq_debug_linear16_forms(9, 64, 64, 3)) == 1
+    assert S.svdq_debug_linear16_forms(0, 64, 64) == [] and S.svdq_debug_linear16_forms(64, 64, 64, 4) == []
+    assert S.lib().svdq_debug_linear16_forms(64, 64, 64, 0, None) == 0
+
+
 def norm(dtype=0, pt=0, M=4, K=64, X=A, ldx=64, w=B, ldw=64, b=C, ldb=64, off=0.0, rpg=2, eps=1e-6,
          Y=D, ldy=64, mean=None, rstd=None):
     return S.lib().svdq_layer_norm(dtype, pt, M, K, X, ldx, w, ldw, b, ldb, off, rpg, eps, Y, ldy, mean,

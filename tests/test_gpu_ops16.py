@@ -364,6 +364,60 @@ def test_linear_backward_long(M, K, N, dtype):
     check_linear_bwd(M, K, N, dtype, S.EPI_GELU, seed=8)
 
 
+# Sizes for which between them every form of a product is chosen (which the CPU
+# tests check): forward, dX alone, dW alone, both in one launch or in two.
+FORM_SIZES = {
+    0: [(20, 42, 41), (285, 967, 386), (29, 1159, 41), (17, 42, 4939), (531, 1643, 501), (261, 1205, 398), (47, 3950, 42),
+        (19, 42, 9476), (539, 2300, 972), (404, 2225, 580), (313, 4357, 393), (9877, 41, 131), (2074, 194, 1046),
+        (1621, 650, 2037)],
+    1: [(9, 46, 41), (391, 580, 919), (294, 329, 586), (13, 42, 834), (9, 9569, 44), (541, 897, 2276), (526, 524, 2209),
+        (284, 349, 4524), (129, 9585, 50), (1690, 1286, 658)],
+    2: [(9, 46, 41), (877, 605, 397), (611, 342, 273), (463, 42, 44), (9, 9569, 44), (2377, 947, 531), (2340, 479, 515),
+        (4581, 321, 292), (12, 131, 9510), (645, 1258, 1813)],
+    3: [(9, 46, 41), (65, 45, 1094), (196, 46, 605), (482, 41, 476), (11, 4817, 41), (87, 137, 2958), (205, 65, 2198),
+        (9, 9569, 44), (654, 2757, 43),
+        # two launches
+        (16, 64, 12288), (67, 74, 5182), (40, 1103, 8924), (60, 2692, 8797), (687, 245, 5347), (7711, 3470, 194),
+        (12, 4881, 4461), (260, 333, 2913), (2199, 45, 7330), (266, 340, 3670), (12, 2449, 3359), (587, 946, 9051),
+        (539, 452, 4116), (158, 513, 4380), (649, 131, 9811), (4562, 1022, 290), (9449, 461, 92), (8879, 974, 586),
+        (13833, 964, 78)],
+}
+
+
+@pytest.mark.parametrize("gradients,M,K,N", [(w, *size) for w, sizes in FORM_SIZES.items() for size in sizes])
+def test_linear_every_form(gradients, M, K, N):
+    for dtype in (BF16, F16):
+        if gradients == 0:
+            check_linear(M, K, N, dtype, S.EPI_GELU, seed=M)
+        else:
+            check_linear_bwd(M, K, N, dtype, S.EPI_NONE, seed=M, want=(bool(gradients & 1), bool(gradients & 2), False))
+            check_linear_bwd(M, K, N, dtype, S.EPI_GELU, seed=K, want=(bool(gradients & 1), bool(gradients & 2), True))
+
+
+@pytest.mark.parametrize("M,K,N", [(16, 64, 12288), (260, 333, 2913), (587, 946, 9051)])
+def test_linear_backward_two_launches_replayed(M, K, N):
+    """Two products behind one another, eager, captured and replayed: the same bits."""
+    assert len(S.svdq_debug_linear16_forms(M, K, N, 3)) == 2
+    g = gen(M)
+    X, W, dY = rows(g, M, K, F16), rows(g, N, K, F16, 0.1), rows(g, M, N, F16)
+    dX, dW, db = out(M, K, F16), out(N, K, F16), torch.empty((N,), dtype=F16, device="cuda")
+    ws = torch.empty((S.svdq_linear16_backward_workspace(M, K, N, S.EPI_NONE),), dtype=torch.uint8, device="cuda")
+    call = lambda: S.svdq_linear16_backward(dY, X, W, None, dX, dW, db, ws)
+    call()
+    want = [t.clone() for t in (dX, dW, db)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call()
+    for again in (graph.replay, call, graph.replay):
+        for t in (dX, dW, db, ws):
+            t.fill_(7)
+        again()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((dX, dW, db), want))
+    S.svdq_get_op_error()
+
+
 @pytest.mark.parametrize("want", [(True, False, False), (False, True, False), (False, False, True)])
 @pytest.mark.parametrize("epi", [S.EPI_NONE, S.EPI_SILU])
 def test_linear_backward_parts(want, epi):

@@ -42,7 +42,7 @@ __all__ = [
     "svdq_linear_quantize_next", "svdq_linear_quantize_next_workspace", "SVDQMLP",
     "svdq_linear_host", "svdq_linear_host_workspace",
     "EPI_SILU", "svdq_linear16", "svdq_linear16_backward", "svdq_linear16_backward_workspace",
-    "svdq_get_op_error", "svdq_layer_norm", "svdq_layer_norm_backward",
+    "svdq_debug_linear16_forms", "svdq_get_op_error", "svdq_layer_norm", "svdq_layer_norm_backward",
     "svdq_layer_norm_backward_workspace", "ROPE_INTERLEAVED", "ROPE_HALVES", "RopePlan",
     "svdq_rope_create", "svdq_rope", "rope_frequencies", "Linear16", "LayerNorm", "SVDQQKV",
 ]
@@ -135,6 +135,7 @@ def lib() -> ctypes.CDLL:
         "svdq_linear16_backward_workspace": (ctypes.c_size_t, [_i, _i, _i, _i]),
         "svdq_linear16_backward": (_i, [_i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _i,
                                         _vp, _i, _vp, _i, _vp, _vp, ctypes.c_size_t, _vp]),
+        "svdq_debug_linear16_forms": (_i, [_i, _i, _i, _i, _vp]),
         "svdq_get_op_error": (_i, [_vp]),
         "svdq_layer_norm": (_i, [_i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _i, ctypes.c_float, _i,
                                  ctypes.c_float, _vp, _i, _vp, _vp, _vp]),
@@ -540,6 +541,15 @@ def svdq_linear16_backward(dY, X, W, preact, dX, dW, dbias, workspace, epilogue=
                                                   None if stream is None else stream.cuda_stream)
     if rc:
         raise SVDQError(rc, "svdq_linear16_backward")
+
+
+def svdq_debug_linear16_forms(M: int, K: int, N: int, gradients: int = 0) -> list:
+    """Test hook, host only: the forms (on CTA pairs, tile columns, splits of the
+    reduction) of a 16-bit product's launches; gradients: 0 forward, 1 dX, 2 dW,
+    3 both.  Empty for the few rows that take another way."""
+    f = (ctypes.c_int * 6)()
+    n = lib().svdq_debug_linear16_forms(int(M), int(K), int(N), int(gradients), f)
+    return [(bool(f[3 * i]), f[3 * i + 1], f[3 * i + 2]) for i in range(n)]
 
 
 def svdq_get_op_error(stream=None):

@@ -209,27 +209,50 @@ G16Choice choose_gemm16(const G16Launch& l) {
   return best;
 }
 
-cudaError_t launch_gemm(G16Launch& l, cudaStream_t st) {
-  l.err = op_err_address();
-  if (!l.err) return cudaErrorInvalidDevice;
-  const auto launch = [&](const G16Launch& k, const G16Choice& c) {
-    return c.pair ? launch_gemm16_pair(k, c.bn, st) : launch_gemm16_split(k, c.bn, c.splits, st);
-  };
+// The launches of a call and their forms.
+struct G16Plan {
+  int launches;
+  G16Launch l[2];
+  G16Choice c[2];
+};
+
+G16Plan plan_gemm(const G16Launch& l) {
   // Two launches where the two gradients want different forms (16 x 64 to
   // 12288: 16.5 us, 52 in one launch; 16 x 1152 to 4608: 23, 28) and the model
   // puts their sum a tenth lower: one launch fills the GPU better and saves the
   // second start (16 x 512 to 512: 6.9 us, 10.6 in two launches).
   const G16Choice both = choose_gemm16(l);
   if (l.A[0].p && l.A[1].p) {
-    G16Launch one[2] = {l, l};
-    one[0].A[1].p = one[1].A[0].p = nullptr;
-    const G16Choice c[2] = {choose_gemm16(one[0]), choose_gemm16(one[1])};
-    if (c[0].us + c[1].us < 0.9 * both.us) {
-      const cudaError_t e = launch(one[0], c[0]);
-      return e != cudaSuccess ? e : launch(one[1], c[1]);
-    }
+    G16Plan two{2, {l, l}, {}};
+    two.l[0].A[1].p = two.l[1].A[0].p = nullptr;
+    for (int i = 0; i < 2; ++i) two.c[i] = choose_gemm16(two.l[i]);
+    if (two.c[0].us + two.c[1].us < 0.9 * both.us) return two;
   }
-  return launch(l, both);
+  return {1, {l, l}, {both, both}};
+}
+
+cudaError_t launch_gemm(G16Launch& l, cudaStream_t st) {
+  l.err = op_err_address();
+  if (!l.err) return cudaErrorInvalidDevice;
+  const G16Plan plan = plan_gemm(l);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < plan.launches && e == cudaSuccess; ++i) {
+    const G16Choice& c = plan.c[i];
+    e = c.pair ? launch_gemm16_pair(plan.l[i], c.bn, st) : launch_gemm16_split(plan.l[i], c.bn, c.splits, st);
+  }
+  return e;
+}
+
+// The operands of the gradients' products, dX at 0 and dW at 1.
+void set_gradient(G16Launch& l, int i, const void* dP, long long lddp, const void* other, long long ldo, int M,
+                  int K, int N) {
+  if (i == 0) {
+    l.A[0] = {dP, lddp, M, N, false};
+    l.B[0] = {other, ldo, K, N, true};
+  } else {
+    l.A[1] = {dP, lddp, N, M, true};
+    l.B[1] = {other, ldo, K, M, true};
+  }
 }
 
 // Workspace of a backward call: dP of an activation, then the partial column
@@ -412,17 +435,39 @@ svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* d
   svdq::G16Launch l{};
   l.kind = svdq::G16Kind::Gradients;
   l.bf16 = bf16;
-  auto set = [&](int i, const svdq::Operand& A, const svdq::Operand& B, void* out, int ld) {
-    l.A[i] = A;
-    l.B[i] = B;
+  auto set = [&](int i, const void* other, int ldo, void* out, int ld) {
+    svdq::set_gradient(l, i, dP, lddp, other, ldo, M, K, N);
     l.o[i].out = static_cast<uint16_t*>(out);
     l.o[i].ldo = ld;
     l.o[i].epilogue = SVDQ_EPI_NONE;
     l.o[i].bf16 = bf16;
   };
-  if (dX) set(0, {dP, lddp, M, N, false}, {W, ldw, K, N, true}, dX, lddx);
-  if (dW) set(1, {dP, lddp, N, M, true}, {X, ldx, K, M, true}, dW, lddw);
+  if (dX) set(0, W, ldw, dX, lddx);
+  if (dW) set(1, X, ldx, dW, lddw);
   return svdq::status_of(dX || dW ? svdq::launch_gemm(l, stream) : cudaSuccess);
+}
+
+int svdq_debug_linear16_forms(int M, int K, int N, int gradients, int forms[2][3]) {
+  if (M < 1 || K < 1 || N < 1 || !svdq::sizes_fit(M, K, N) || gradients < 0 || gradients > 3 || !forms) return 0;
+  if (M <= (gradients ? svdq::THIN_BWD_ROWS : svdq::THIN_ROWS)) return 0;
+  svdq::G16Launch l{};
+  const void* there = &l;      // the choice goes by sizes, and by which operands there are
+  if (gradients) {
+    l.kind = svdq::G16Kind::Gradients;
+    for (int i = 0; i < 2; ++i)
+      if (gradients >> i & 1) svdq::set_gradient(l, i, there, N, there, K, M, K, N);
+  } else {
+    l.kind = svdq::G16Kind::Forward;
+    l.A[0] = {there, K, M, K, false};
+    l.B[0] = {there, K, N, K, false};
+  }
+  const svdq::G16Plan plan = svdq::plan_gemm(l);
+  for (int i = 0; i < plan.launches; ++i) {
+    forms[i][0] = plan.c[i].pair;
+    forms[i][1] = plan.c[i].bn;
+    forms[i][2] = plan.c[i].splits;
+  }
+  return plan.launches;
 }
 
 svdq_status svdq_get_op_error(cudaStream_t stream) {
