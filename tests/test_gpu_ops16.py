@@ -527,6 +527,19 @@ def test_norm_sizes(M, K, dtype, pt):
     check_norm(M, K, dtype, pt, seed=M + K)
 
 
+# the longest row of each way to hold one (16-byte vectors of a row), and one a little shorter
+@pytest.mark.parametrize("vectors", [8, 16, 32, 64, 96, 128, 160, 256, 384, 512, 640, 768, 1024, 1280, 1536, 2048, 2560,
+                                     3072, 3584, 4096])
+def test_norm_every_row_form(vectors):
+    for dtype, pt in ((BF16, BF16), (F16, F32), (F32, F32)):
+        v = 128 // torch.finfo(dtype).bits
+        for K in (vectors * v, vectors * v - 3):
+            if K <= 16384:
+                check_norm(37, K, dtype, pt, 2, 1.0, seed=K)
+                check_norm_bwd(37, K, dtype, pt, 2, 1.0, seed=K)
+                check_norm_bwd(37, K, dtype, pt, want=(True, False, False), seed=K)
+
+
 @pytest.mark.parametrize("M,K,groups", [(8, 72, 8), (10, 1152, 3), (1000, 136, 4), (7, 4608, 7), (5, 520, 2),
                                         (103, 24, 13), (1001, 60, 3), (999, 125, 2)])
 @pytest.mark.parametrize("off", [0.0, 1.0])
