@@ -559,8 +559,9 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
 /*
  * Gradients of svdq_linear16 for the output gradient dY [M][lddy]:
  *   dP = dY epi'(P) (rounded to `dtype`, the operand type of the products,
- *        but for up to 8 rows, whose products run in fp32; dP = dY when
- *        epilogue is NONE),
+ *        but for up to 8 rows, whose products run in fp32: without that
+ *        rounding the error of dX and dW is their own rounding's, with it 1.4
+ *        times as much; dP = dY when epilogue is NONE),
  *   dX [M][lddx] = dP W,  dW [N][lddw] = dP^T X,  db [N] = sum_m dP (of the
  *   fp32 values).  R's gradient is dY itself and is not copied.
  * dX, dW and db may each be NULL (not computed); X is needed for dW only

@@ -2,12 +2,12 @@
 //
 // A row belongs to one team (a quarter of a warp for the shortest rows, a
 // warp, or a block of 128, 256 or 512 threads for long ones), and a team walks
-// over rows of one group, one to four at a time.  Each thread copies its own 16-byte vectors of the next rows to its own places in
-// shared memory (cp.async, no barrier), so that the bytes in flight do not
-// depend on the registers that a row needs; the group's scale (with its
-// offset) and shift wait there too, in fp32, converted once per block.
-// Arithmetic runs on pairs (packed fp32 instructions), which keeps it below
-// the memory time.
+// over rows of one group, one to four at a time.  Each thread copies its own
+// 16-byte vectors of the next rows to its own places in shared memory
+// (cp.async, no barrier), so that the bytes in flight do not depend on the
+// registers that a row needs; the group's scale (with its offset) and shift
+// wait there too, in fp32, converted once per block.  Arithmetic runs on pairs
+// (packed fp32 instructions), which keeps it below the memory time.
 //
 // Forward: the variance is the two-pass one, sum (x - mu)^2 in fp32 after the
 // mean, from registers (no cancellation for rows with a large mean).  The mean

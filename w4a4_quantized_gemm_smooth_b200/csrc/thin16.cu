@@ -4,10 +4,11 @@
 // Bound by reading W once, so nothing is staged: a block owns 8 rows of W
 // (output columns), its eight warps share out the reduction, and every thread
 // loads 16 bytes of its rows of W and of X straight into the fragments of
-// mma.sync m16n8k16 (X as the 16-row operand, eight rows of W as the other).  A thread's eight consecutive elements go to two products as
-// (0, 1, 2, 3) and (4, 5, 6, 7), in W and X alike: the order of the reduction
-// inside a run does not matter, and both operands keep it.  The warps' sums
-// meet in shared memory, in order.
+// mma.sync m16n8k16 (X as the 16-row operand, eight rows of W as the other).  A
+// thread's eight consecutive elements go to two products as (0, 1, 2, 3) and
+// (4, 5, 6, 7), in W and X alike: the order of the reduction inside a run does
+// not matter, and both operands keep it.  The warps' sums meet in shared memory,
+// in order.
 //
 // The fifth-generation tensor cores would take 128 rows for one, and a tile's
 // way through TMA, shared memory and TMEM costs 4 us before the first byte of
