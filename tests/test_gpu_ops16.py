@@ -450,6 +450,27 @@ def test_linear_backward_of_an_empty_batch_is_zero():
     assert bool((dW == 0).all()) and bool((db == 0).all()) and padding_kept(dW)
 
 
+def test_linear_layer_with_another_weight():
+    """A layer whose weight, type, bias or epilogue has been exchanged since the
+    last call of as many rows: its buffers follow."""
+    g = gen(12)
+    layer = S.Linear16(rows(g, 48, 64, BF16, 0.1), None)
+    for N, K, dtype, epi, bias in ((48, 64, BF16, S.EPI_NONE, False), (48, 64, F16, S.EPI_NONE, True), (80, 64, F16, S.EPI_GELU, True),
+                                   (80, 40, F16, S.EPI_NONE, True), (48, 40, BF16, S.EPI_SILU, False), (48, 40, BF16, S.EPI_SILU, True)):
+        layer.weight, layer.epilogue = rows(g, N, K, dtype, 0.1), epi
+        layer.bias = torch.randn((N,), generator=g, device="cuda").to(dtype) if bias else None
+        X, dY = rows(g, 20, K, dtype), rows(g, 20, N, dtype)
+        Y = layer(X, save=True)
+        want = torch.empty((20, N), dtype=dtype, device="cuda")
+        S.svdq_linear16(X, layer.weight, want, layer.bias, epilogue=epi)
+        assert torch.equal(Y, want)
+        dX, dW, db = layer.backward(dY)
+        assert dX.shape == X.shape and dW.shape == layer.weight.shape and dX.dtype == dW.dtype == dtype
+        assert (db is not None) == bias and (db is None or (db.shape == (N,) and db.dtype == dtype))
+        ref = (dY.double() * act_grad64(layer.P.double() if epi else dY.double(), epi)).T @ X.double()
+        assert float((dW.double() - ref).norm() / ref.norm()) <= 2 * half(dtype)
+
+
 def test_linear_gradients_against_differences():
     """Central differences of the 64-bit loss sum(Y dY) through the GPU's own
     forward pass would drown in 16-bit steps, so the differences are of the

@@ -736,13 +736,13 @@ class Linear16:
     forward(X) returns epi(X W^T + b) + residual on the current stream; with
     save=True it keeps X and the pre-activation for backward(dY), which
     returns (dX, dW, db); X is kept by reference and has to stay as it is until
-    then.  Buffers are reallocated only when M changes, and the next call
-    reuses them.
+    then.  Buffers are reallocated only when M, the weight's shape, the type or
+    the device changes, and the next call reuses them.
     """
 
     def __init__(self, weight, bias=None, epilogue: int = EPI_NONE):
         self.weight, self.bias, self.epilogue = weight, bias, epilogue
-        self._M = self._Mb = -1
+        self._key = self._keyb = None
         self.Y = self.P = self._saved = None
 
     @staticmethod
@@ -752,8 +752,9 @@ class Linear16:
 
     def forward(self, X, residual=None, out=None, save: bool = False):
         M, N = X.shape[0], self.weight.shape[0]
-        if M != self._M:
-            self.Y, self.P, self._M = self._empty(M, N, X), None, M
+        key = (M, N, X.dtype, X.device)
+        if key != self._key:
+            self.Y, self.P, self._key = self._empty(M, N, X), None, key
         if save and self.epilogue != EPI_NONE and self.P is None:
             self.P = self._empty(M, N, X)
         Y = self.Y if out is None else out
@@ -769,12 +770,13 @@ class Linear16:
             raise RuntimeError("backward needs a forward call with save=True")
         X, W = self._saved, self.weight
         M, (N, K) = X.shape[0], W.shape
-        if M != self._Mb:
+        key = (M, N, K, X.dtype, X.device, self.bias is None, self.epilogue)
+        if key != self._keyb:
             n = svdq_linear16_backward_workspace(M, K, N, self.epilogue)
             self.ws = torch.empty((n,), dtype=torch.uint8, device=X.device)
             self.dX, self.dW = self._empty(M, K, X), self._empty(N, K, X)
             self.db = None if self.bias is None else torch.empty_like(self.bias)
-            self._Mb = M
+            self._keyb = key
         svdq_linear16_backward(dY, X, W, self.P if self.epilogue != EPI_NONE else None, self.dX,
                                self.dW, self.db, self.ws, self.epilogue)
         return self.dX, self.dW, self.db
@@ -793,8 +795,8 @@ class LayerNorm:
     that all groups share, [K] or [1, K], is summed over them).  X is kept by
     reference and has to stay as it is until then, so with save=True out cannot
     be X (ValueError); without it the norm may run in place.  Buffers are
-    reallocated only when X's shape or type changes, and the next call reuses
-    them.
+    reallocated only when X's shape, type or device changes, and the next call
+    reuses them.
     """
 
     def __init__(self, weight=None, bias=None, eps: float = 1e-6, weight_offset: float = 0.0):
@@ -805,11 +807,12 @@ class LayerNorm:
     def forward(self, X, out=None, rows_per_group: int = 0, save: bool = False):
         import torch
         M, K = X.shape
-        if (M, K, X.dtype) != self._key:
+        key = (M, K, X.dtype, X.device)
+        if key != self._key:
             self.Y = Linear16._empty(M, K, X)
             self.mean = torch.empty((M,), dtype=torch.float32, device=X.device)
             self.rstd = torch.empty_like(self.mean)
-            self._key = (M, K, X.dtype)
+            self._key = key
         Y = self.Y if out is None else out
         if save and X.numel() and Y.data_ptr() == X.data_ptr():
             raise ValueError("save=True keeps X for backward: out cannot be X itself")
@@ -825,7 +828,7 @@ class LayerNorm:
         X, rpg = self._saved
         M, K = X.shape
         w, b = self.weight, self.bias
-        key = (M, K, X.dtype, rpg, *((p.shape, p.dtype) for p in (w, b) if p is not None))
+        key = (M, K, X.dtype, X.device, rpg, *((p.shape, p.dtype) for p in (w, b) if p is not None))
         if key != self._keyb:
             n = max(svdq_layer_norm_backward_workspace(M, K, r) for r in (0, rpg))
             self.ws = torch.empty((n,), dtype=torch.uint8, device=X.device) if n else None
