@@ -1087,6 +1087,61 @@ def test_epilogue_past_32_bits_is_refused():
         S.svdq_linear16(X, W, Y, epilogue=1 << 64)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in an operand: the last rows are what they are
+    by themselves (norm, rotation), or what 64 bits give (products)."""
+    g = gen(81)
+    M, K = 140000, 16384
+    X = torch.randn((M, K), generator=g, device="cuda", dtype=BF16)
+    Y = torch.empty_like(X)
+    mean, rs = torch.empty((M,), device="cuda"), torch.empty((M,), device="cuda")
+    S.svdq_layer_norm(X, Y, mean=mean, rstd=rs)
+    last = torch.empty((50, K), dtype=BF16, device="cuda")
+    S.svdq_layer_norm(X[-50:], last)
+    assert torch.equal(Y[-50:], last)
+    S.svdq_layer_norm_backward(X, X, mean, rs, Y)
+    S.svdq_layer_norm_backward(X[-50:], X[-50:], mean[-50:], rs[-50:], last)
+    assert torch.equal(Y[-50:], last)
+    plan = S.svdq_rope_create([64], S.rope_frequencies([64]))
+    heads = lambda t: t.unflatten(1, (128, 128))
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")[:, None]
+    S.svdq_rope(plan, pos, heads(X), heads(Y))
+    S.svdq_rope(plan, pos[-50:], heads(X[-50:]), heads(last))
+    assert torch.equal(Y[-50:], last)
+    # products: rows of X and dX, then rows of W and dW, past that limit
+    h = half(BF16)
+    W, dY = rows(g, 24, K, BF16, K ** -0.5), rows(g, M, 24, BF16)
+    Z, dW, db = out(M, 24, BF16), out(24, K, BF16), torch.empty((24,), dtype=BF16, device="cuda")
+    ws = torch.empty((S.svdq_linear16_backward_workspace(M, K, 24),), dtype=torch.uint8, device="cuda")
+    S.svdq_linear16(X, W, Z)
+    S.svdq_linear16_backward(dY, X, W, None, Y, dW, db, ws)
+    x, w, d = X[-50:].double(), W.double(), dY[-50:].double()
+    e = K * 2.0 ** -24 * (x.abs() @ w.abs().T)
+    close(Z[-50:], x @ w.T, h * ((x @ w.T).abs() + e) + e, "Y")
+    e = 24 * 2.0 ** -24 * (d.abs() @ w.abs())
+    close(Y[-50:], d @ w, h * ((d @ w).abs() + e) + e, "dX")
+    dw, mag = torch.zeros((24, K), dtype=torch.float64, device="cuda"), torch.zeros((24, K), dtype=torch.float64, device="cuda")
+    for i in range(0, M, 10000):
+        p, q = dY[i:i + 10000].double().T, X[i:i + 10000].double()
+        dw += p @ q
+        mag += p.abs() @ q.abs()
+    e = M * 2.0 ** -24 * mag
+    close(dW, dw, h * (dw.abs() + e) + e, "dW")
+    for rows_ in (3, 20):
+        A = rows(g, rows_, K, BF16)
+        V = torch.empty((rows_, M), dtype=BF16, device="cuda")
+        S.svdq_linear16(A, X, V)                                    # X as the weight
+        e = K * 2.0 ** -24 * (A.double().abs() @ x.abs().T)
+        ref = A.double() @ x.T
+        close(V[:, -50:], ref, h * (ref.abs() + e) + e, "Y")
+        G = torch.randn((rows_, M), generator=g, device="cuda").to(BF16)
+        S.svdq_linear16_backward(G, A, X, None, None, Y, None, None)
+        ref = G[:, -50:].double().T @ A.double()
+        e = rows_ * 2.0 ** -24 * (G[:, -50:].double().abs().T @ A.double().abs())
+        close(Y[-50:], ref, h * (ref.abs() + e) + e, "dW")
+    S.svdq_get_op_error()
+
+
 def test_binding_through_torchs_public_functions():
     """The calls find the device and the current stream through what stands in
     for the private functions where a torch lacks them."""
