@@ -570,7 +570,8 @@ svdq_status svdq_linear16(int dtype, int M, int K, int N, const void* X, int ldx
  * Results do not depend on timing: every sum has a fixed order.
  * workspace: device memory, 256-byte aligned, of at least
  * svdq_linear16_backward_workspace(M, K, N, epilogue) bytes (may be 0), which
- * is enough for any choice of gradients; it needs no initialisation.
+ * is enough for any choice of gradients (fewer rows may need more); it needs
+ * no initialisation.
  */
 size_t svdq_linear16_backward_workspace(int M, int K, int N, int epilogue);
 svdq_status svdq_linear16_backward(int dtype, int M, int K, int N, const void* dY, int lddy,

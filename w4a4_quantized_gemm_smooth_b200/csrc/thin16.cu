@@ -14,8 +14,8 @@
 // way through TMA, shared memory and TMEM costs 4 us before the first byte of
 // the result leaves.
 //
-// One row of 12288 to 4608: 18.9 us, 6.0 TB/s; 8 rows 19.4, 16 rows 35 us (the
-// tcgen05 kernels: 41).  One row of 4608 to 21504: 34 us, 5.8 TB/s; of 1152 to
+// One row of 12288 to 4608: 19.3 us, 5.9 TB/s; 8 rows 20.2, 16 rows 35 us (the
+// tcgen05 kernels: 41).  One row of 4608 to 21504: 35 us, 5.7 TB/s; of 1152 to
 // 6912: 5.9 us (8.7).  Four runs in flight measured best (three 20.8 us, five
 // 20.0, eight 24.7 for the first size: more loads per thread, fewer threads);
 // 16 or 32 rows of W a block were slower (22.8 us and more).
@@ -52,13 +52,13 @@ __device__ __forceinline__ void mma_thin(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes that no other thread reads: an ordinary, coherent load that leaves
-// the first-level cache to X.  It also stays where it stands, in a batch of U:
-// with loads that the compiler may move the batch comes apart (one row of 12288
-// to 4608 26.3 us, 18.9 with this one; past that cache for X too, 20.8).
-__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
+// An ordinary, coherent load of 16 bytes that stays where it stands, in a batch
+// of U: with loads that the compiler may move the batch comes apart (one row of
+// 12288 to 4608 26.3 us, 19.3 with this one).  Past the first-level cache that
+// size takes 19.0 us, but 1152 to 6912, call by call from L2, 5.4 instead of 4.7.
+__device__ __forceinline__ uint4 load_here(const uint16_t* p) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -92,7 +92,7 @@ thin16_kernel(const ThinArgs a) {
     for (int u = 0; u < U; ++u) {
       const int k = 32 * (r0 + u);
       if (r0 + u < end) {
-        wq[u] = load_once(w + k);
+        wq[u] = load_here(w + k);
 #pragma unroll
         for (int j = 0; j < XT; ++j) xq[u][j] = *reinterpret_cast<const uint4*>(x[j] + k);
       }
