@@ -548,13 +548,15 @@ def test_norm_sizes(M, K, dtype, pt):
     check_norm(M, K, dtype, pt, seed=M + K)
 
 
-# the longest row of each way to hold one (16-byte vectors of a row), and one a little shorter
-@pytest.mark.parametrize("vectors", [8, 16, 32, 64, 96, 128, 160, 256, 384, 512, 640, 768, 1024, 1280, 1536, 2048, 2560,
-                                     3072, 3584, 4096])
-def test_norm_every_row_form(vectors):
+# the longest row of each way to hold one (threads to a row, 16-byte vectors to
+# a thread), and one a little shorter
+@pytest.mark.parametrize("team,vectors", [(8, 1), (16, 1), (32, 1), (32, 2), (32, 3), (32, 4), (32, 5), (128, 2), (128, 3),
+                                          (128, 4), (128, 5), (256, 3), (256, 4), (256, 5), (512, 3), (512, 4), (512, 5),
+                                          (512, 6), (512, 7), (512, 8)])
+def test_norm_every_row_form(team, vectors):
     for dtype, pt in ((BF16, BF16), (F16, F32), (F32, F32)):
-        v = 128 // torch.finfo(dtype).bits
-        for K in (vectors * v, vectors * v - 3):
+        v = 128 // torch.finfo(dtype).bits * team * vectors
+        for K in (v, v - 3):
             if K <= 16384:
                 check_norm(37, K, dtype, pt, 2, 1.0, seed=K)
                 check_norm_bwd(37, K, dtype, pt, 2, 1.0, seed=K)
