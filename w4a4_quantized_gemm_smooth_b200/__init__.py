@@ -485,7 +485,8 @@ def svdq_debug_partials(w: Weights, M, xq, row0, nrows, col0, ncols, P, stream=N
 # ------------------------------------------------------------------------
 # 16-bit operators around the quantised layers.  These calls take plain
 # tensors, so the binding checks each one's device, type and shape before it
-# passes the pointer on (ValueError); the library checks sizes and alignment.
+# passes the pointer on (ValueError); the library checks sizes, alignment and
+# overlap (SVDQError).
 # They go through a small CPython module, since a call through ctypes takes
 # the host longer than one token's kernels take the device.
 
